@@ -20,6 +20,11 @@ pointers:
     w8_quantize(A, fmt, col=None, col_op=W8_COL_NONE) -> (q, scale)
     w8_gemm(Xq, x_scale, Wq, w_scale, fmt, dtype) -> Y
     w8a8_linear(X, Wq, w_scale, fmt, s=None) -> Y
+    w4kv_cache_empty(num_pages, page_size, kv_heads, head_dim, fmt, device) -> W4KVCache
+    w4kv_append(K, V, cache, page_table, kv_lens, cu_rows)
+    w4kv_read(cache, page_table, kv_lens, cu_rows, rows, dtype) -> (K, V)
+    w4kv_attention(Q, cache, page_table, kv_lens, cu_rows, max_rows=None, scale=None,
+                   causal=True, window=0, return_lse=False) -> O[, lse]
     w4_status_string(status) -> str
     w4_device_status(reset=True) -> int
 """
@@ -40,7 +45,8 @@ __all__ = [
     "W8_COL_DIV",
     "Workspace", "W4_OK", "W4_ERR_INVALID_ARG", "W4_ERR_UNSUPPORTED", "W4_ERR_CUDA",
     "W4_ERR_TIMEOUT", "W4_ERR_BOUNDS", "W4_F16", "W4_BF16", "w4_debug_build",
-    "w4_debug_first_failure",
+    "w4_debug_first_failure", "W4KVCache", "w4kv_cache_empty", "w4kv_append", "w4kv_read",
+    "w4kv_attention", "w4kv_attention_workspace_bytes", "W4KV_INT8", "W4KV_E4M3", "W4KV_INT4",
 ]
 
 W4_OK, W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED, W4_ERR_CUDA, W4_ERR_TIMEOUT = 0, 1, 2, 3, 4
@@ -48,12 +54,28 @@ W4_ERR_BOUNDS = 5
 W4_F16, W4_BF16 = 0, 1
 W8_INT8, W8_E4M3 = 0, 1
 W8_COL_NONE, W8_COL_MUL, W8_COL_DIV = 0, 1, 2
+W4KV_INT8, W4KV_E4M3, W4KV_INT4 = 0, 1, 2
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # W4_DEBUG=1 in the environment selects the build with in-kernel bounds checks
 lib_path = os.path.join(_PKG, "lib", "libw4a16_debug.so" if os.environ.get("W4_DEBUG") == "1"
                         else "libw4a16.so")
 _lib = None
+
+
+class _CCache(ctypes.Structure):
+    """w4kv_cache of include/w4kv.h"""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("fmt", ctypes.c_int)]
+
+
+class _CBatch(ctypes.Structure):
+    """w4kv_batch of include/w4kv.h"""
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_width", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
+                ("cu_rows", ctypes.c_void_p), ("batch", ctypes.c_int64)]
 
 
 class W4Error(RuntimeError):
@@ -120,6 +142,16 @@ def load() -> ctypes.CDLL:
     lib.w8a8_workspace_bytes.restype = SZ
     lib.w8a8_linear.argtypes = [P, I, I64, I64, P, I, P, P, I64, P, P, SZ, P]
     lib.w8a8_linear.restype = I
+    CP, BP = ctypes.POINTER(_CCache), ctypes.POINTER(_CBatch)
+    lib.w4kv_append.argtypes = [CP, BP, P, P, I, I64, I64, I64, I64, I64, P]
+    lib.w4kv_append.restype = I
+    lib.w4kv_read.argtypes = [CP, BP, P, P, I, I64, I64, I64, I64, I64, P]
+    lib.w4kv_read.restype = I
+    lib.w4kv_attention_workspace_bytes.argtypes = [CP, I64, I64, I64, I]
+    lib.w4kv_attention_workspace_bytes.restype = SZ
+    lib.w4kv_attention.argtypes = [CP, BP, P, I, I64, I, I64, I64, P, I64, I64, P, I64, F, I, I64,
+                                   P, SZ, P]
+    lib.w4kv_attention.restype = I
     lib.w4_last_error.argtypes = []
     lib.w4_last_error.restype = ctypes.c_char_p
     _lib = lib
@@ -487,3 +519,184 @@ def w8a8_linear(X, Wq, w_scale, fmt: int, s=None, out=None, workspace=None, stre
     if st != W4_OK:
         raise W4Error("w8a8_linear", st)
     return Y
+
+
+# ---- quantized paged key/value cache -----------------------------------------------------
+
+class W4KVCache:
+    """The tensors of a quantized paged cache (layout: include/w4kv.h).
+
+    k_codes, v_codes   uint8 [num_pages][kv_heads][page_size][head_dim bytes;
+                       head_dim / 2 for W4KV_INT4]
+    k_scales, v_scales float32 [num_pages][kv_heads][page_size]
+
+    The object holds the tensors and nothing else; write into them freely, but
+    do not replace their storage."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, fmt: int):
+        fmt = int(fmt)
+        if fmt not in (W4KV_INT8, W4KV_E4M3, W4KV_INT4):
+            raise ValueError("fmt must be W4KV_INT8, W4KV_E4M3 or W4KV_INT4")
+        _check_dev(k_codes, k_scales, v_codes, v_scales)
+        if k_codes.dim() != 4 or k_codes.dtype != torch.uint8 or v_codes.dtype != torch.uint8:
+            raise ValueError("codes must be uint8 [pages][kv_heads][page_size][row bytes]")
+        if v_codes.shape != k_codes.shape:
+            raise ValueError("k_codes and v_codes must have one shape")
+        for t in (k_scales, v_scales):
+            if t.dtype != torch.float32 or t.shape != k_codes.shape[:3]:
+                raise ValueError("scales must be float32 [pages][kv_heads][page_size]")
+        if len({t.device for t in (k_codes, k_scales, v_codes, v_scales)}) != 1:
+            raise ValueError("the cache's tensors must live on one device")
+        self.k_codes, self.k_scales = k_codes, k_scales
+        self.v_codes, self.v_scales = v_codes, v_scales
+        self.fmt, self.device = fmt, k_codes.device
+        self.num_pages, self.kv_heads, self.page_size, row = k_codes.shape
+        self.head_dim = 2 * row if fmt == W4KV_INT4 else row
+        self._c = _CCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                          v_scales.data_ptr(), self.num_pages, self.page_size, self.kv_heads,
+                          self.head_dim, fmt)
+
+
+def w4kv_cache_empty(num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int,
+                     device="cuda") -> W4KVCache:
+    """A cache of zeros: num_pages pages of page_size tokens (a multiple of 16)."""
+    row = head_dim // 2 if fmt == W4KV_INT4 else head_dim
+    shape = (num_pages, kv_heads, page_size)
+    return W4KVCache(*(torch.zeros(s, dtype=d, device=device) for s, d in
+                       ((shape + (row,), torch.uint8), (shape, torch.float32)) * 2), fmt)
+
+
+def _kv_batch(cache, page_table, kv_lens, cu_rows):
+    dev = cache.device
+    for t, name in ((page_table, "page_table"), (kv_lens, "kv_lens"), (cu_rows, "cu_rows")):
+        if t.dtype != torch.int32 or t.device != dev:
+            raise ValueError(f"{name} must be an int32 tensor on the cache's device")
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [batch][pages] with adjacent pages in a row")
+    B = page_table.shape[0]
+    if kv_lens.shape != (B,) or cu_rows.shape != (B + 1,):
+        raise ValueError("kv_lens must be [batch] and cu_rows [batch + 1]")
+    if not (kv_lens.is_contiguous() and cu_rows.is_contiguous()):
+        raise ValueError("kv_lens and cu_rows must be contiguous")
+    return _CBatch(page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+                   kv_lens.data_ptr(), cu_rows.data_ptr(), B)
+
+
+def _kv_rows(t, cache, heads, name):
+    if t.device != cache.device:
+        raise ValueError(f"{name} must live on the cache's device")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.head_dim:
+        raise ValueError(f"{name} must be [rows][{heads}][{cache.head_dim}]")
+    if t.stride(2) != 1:
+        raise ValueError(f"the elements of a row of {name} must be adjacent")
+    return t.stride(0), t.stride(1)
+
+
+def _kv_call(fn, cache, stream, call, made=()):
+    """call(raw stream) with the cache's device current.  `made` are tensors
+    allocated for this call: on an explicit stream the allocator is told."""
+    dev = cache.device
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
+    if dev.index == torch.cuda.current_device():
+        st = call(_stream(stream, dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = call(_stream(stream, dev.index))
+    if st != W4_OK:
+        raise W4Error(fn, st)
+
+
+def w4kv_append(K, V, cache: W4KVCache, page_table, kv_lens, cu_rows, stream=None) -> None:
+    """Quantize the keys and values K, V [rows][kv_heads][head_dim] (strided
+    views welcome) of the last cu_rows[b + 1] - cu_rows[b] tokens of each
+    sequence into the cache.  kv_lens counts them already."""
+    if K.dtype != V.dtype or K.shape[0] != V.shape[0]:
+        raise ValueError("K and V must share one dtype and their number of rows")
+    ks, vs = _kv_rows(K, cache, cache.kv_heads, "K"), _kv_rows(V, cache, cache.kv_heads, "V")
+    b = _kv_batch(cache, page_table, kv_lens, cu_rows)
+    lib = _lib if _lib is not None else load()
+    dt = _dt(K)
+    _kv_call("w4kv_append", cache, stream,
+             lambda s: lib.w4kv_append(cache._c, b, K.data_ptr(), V.data_ptr(), dt, K.shape[0],
+                                       *ks, *vs, s))
+
+
+def w4kv_read(cache: W4KVCache, page_table, kv_lens, cu_rows, rows: int, dtype=torch.float16,
+              out=None, stream=None):
+    """The values of the last cu_rows[b + 1] - cu_rows[b] tokens of each
+    sequence -> (K, V) [rows][kv_heads][head_dim]; `rows` is cu_rows[-1] (rows
+    beyond it are left as they are).  `out` is an optional pair of tensors."""
+    made = ()
+    if out is None:
+        made = out = tuple(torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=dtype,
+                                       device=cache.device) for _ in range(2))
+    K, V = out
+    if K.dtype != V.dtype or K.shape[0] != rows or V.shape[0] != rows:
+        raise ValueError("K and V must share one dtype and have `rows` rows")
+    ks, vs = _kv_rows(K, cache, cache.kv_heads, "K"), _kv_rows(V, cache, cache.kv_heads, "V")
+    b = _kv_batch(cache, page_table, kv_lens, cu_rows)
+    lib = _lib if _lib is not None else load()
+    dt = _dt(K)
+    _kv_call("w4kv_read", cache, stream,
+             lambda s: lib.w4kv_read(cache._c, b, K.data_ptr(), V.data_ptr(), dt, rows, *ks, *vs, s),
+             made)
+    return K, V
+
+
+def w4kv_attention_workspace_bytes(cache: W4KVCache, batch: int, rows: int, max_rows: int,
+                                   heads: int) -> int:
+    return int(load().w4kv_attention_workspace_bytes(cache._c, int(batch), int(rows),
+                                                     int(max_rows), int(heads)))
+
+
+def w4kv_attention(Q, cache: W4KVCache, page_table, kv_lens, cu_rows, max_rows=None, scale=None,
+                   causal: bool = True, window: int = 0, out=None, return_lse: bool = False,
+                   workspace=None, stream=None):
+    """softmax(scale * Q K^T) V of Q [rows][heads][head_dim] over the cached
+    tokens of each row's sequence; scale defaults to head_dim ** -0.5.  causal:
+    a row sees the positions up to its own, the last `window` of them if
+    window > 0.  max_rows is (at least) the longest cu_rows[b + 1] -
+    cu_rows[b]: pass 1 for a decode step; the default is the number of rows.
+    Returns O, or (O, lse) with lse [rows][heads] fp32.
+
+    Scratch space comes from the caching allocator, call by call, unless
+    `workspace` (uint8, w4kv_attention_workspace_bytes bytes, one per call in
+    flight) is given."""
+    rows, heads = Q.shape[0], Q.shape[1]
+    qs = _kv_rows(Q, cache, heads, "Q")
+    dev = cache.device
+    O = out if out is not None else torch.empty((rows, heads, cache.head_dim), dtype=Q.dtype,
+                                                device=dev)
+    if O.dtype != Q.dtype or O.shape[0] != rows:
+        raise ValueError("out must have Q's dtype and rows")
+    os_ = _kv_rows(O, cache, heads, "out")
+    lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
+    b = _kv_batch(cache, page_table, kv_lens, cu_rows)
+    lib = _lib if _lib is not None else load()
+    if max_rows is None:
+        max_rows = max(rows, 1)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    dt = _dt(Q)
+    ws = workspace
+    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+        raise ValueError("workspace must be contiguous on the cache's device")
+    made = [t for t in (None if out is not None else O, lse) if t is not None]
+
+    def call(s):
+        nonlocal ws
+        if ws is None:
+            need = int(lib.w4kv_attention_workspace_bytes(cache._c, b.batch, rows, max_rows, heads))
+            if need:
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+                if stream is not None:
+                    ws.record_stream(stream)
+        return lib.w4kv_attention(cache._c, b, Q.data_ptr(), dt, rows, heads, *qs, O.data_ptr(),
+                                  *os_, _p(lse), int(max_rows), float(scale), int(bool(causal)),
+                                  int(window), _p(ws),
+                                  0 if ws is None else ws.numel() * ws.element_size(), s)
+
+    _kv_call("w4kv_attention", cache, stream, call, made)
+    return (O, lse) if return_lse else O
