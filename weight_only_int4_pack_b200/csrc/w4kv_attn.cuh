@@ -1,0 +1,190 @@
+// w4kv_attn.cuh -- what the attention kernels over the quantized cache share:
+// their arguments, the cut of a call's work into equal contiguous ranges of
+// thread blocks, and the layout of the partial results.
+//
+// Work is counted in units of 128 cached tokens of an item (a key/value head
+// of a sequence; in the tiled kernel, of a tile of its rows).  The units of
+// all items, in the order (sequence, tile, head), are cut into gridDim.x equal
+// ranges; an item that a cut divides is finished by combine_kernel from the
+// partial results of its blocks, in block order (deterministic).  The lengths
+// live on the device, so every block finds its range itself: a block-wide sum
+// over the sequences, then a scan of the 256 that hold its first unit.
+#pragma once
+
+#include "w4kv.cuh"
+
+namespace w4 {
+namespace kv {
+
+constexpr int kUnit = 128;  // cached tokens per unit of work
+
+struct Attn {
+    Cache c;
+    Batch b;
+    const uint16_t *q;
+    int64_t q_row, q_head;
+    uint16_t *o;
+    int64_t o_row, o_head;
+    float *lse;
+    int64_t rows, max_rows;  // rows of the call; rows of a sequence that are served
+    int heads, group;        // query heads; query heads per key/value head
+    float scale_log2;        // scale * log2(e)
+    int causal, window;
+    int64_t min_rows, max_served;  // this launch serves min_rows < rows * group <= max_served
+    uint32_t page_magic;           // floor(2^32 / (page / 16)), for tile / (page / 16)
+    int4 *desc;    // [grid]: the item that starts in a block and ends in a later one
+    float *slots;  // [2 * grid] partial results
+    unsigned *status;
+};
+
+// The rows that a launch serves of a sequence, and the cached positions they see.
+struct Seq {
+    int row0, n;  // first row of the call, rows served (0: not served by this launch)
+    int first;    // position of row0 (negative: sees nothing)
+    int lo, hi;   // cached positions that any of the rows sees: [lo, hi)
+};
+
+// Everything is clamped to the call's rows and to the table; what does not fit is reported.
+__device__ __forceinline__ Seq load_seq(const Attn &a, int b) {
+    Seq s;
+    s.row0 = __ldg(a.b.cu + b);
+    const int end = __ldg(a.b.cu + b + 1), len = __ldg(a.b.lens + b);
+    s.n = end - s.row0;
+    s.first = len - s.n;
+    s.lo = s.hi = 0;
+    if (s.row0 < 0 || end < s.row0 || end > a.rows) {
+        atomicOr(a.status, kStatusBounds);
+        s.n = 0;
+        return s;
+    }
+    if (s.n > a.max_rows) {
+        atomicOr(a.status, kStatusBounds);
+        s.n = static_cast<int>(a.max_rows);
+    }
+    const int64_t tile = int64_t(s.n) * a.group;
+    if (tile <= a.min_rows || tile > a.max_served) {
+        s.n = 0;
+        return s;
+    }
+    s.hi = max(0, a.causal ? min(len, s.first + s.n) : len);
+    const int room = a.b.width * a.c.page;
+    if (s.hi > room) {
+        atomicOr(a.status, kStatusBounds);
+        s.hi = room;
+    }
+    if (a.window > 0) s.lo = min(s.hi, max(0, s.first + 1 - a.window));
+    return s;
+}
+
+// tile / (page / 16) and the remainder.
+__device__ __forceinline__ int page_of_tile(const Attn &a, int tile, int *rest) {
+    const uint32_t d = static_cast<uint32_t>(a.c.page) >> 4;
+    uint32_t q = __umulhi(static_cast<uint32_t>(tile), a.page_magic), r = tile - q * d;
+    if (r >= d) {  // the estimate is at most one short
+        ++q;
+        r -= d;
+    }
+    *rest = static_cast<int>(r);
+    return static_cast<int>(q);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float pow2i(int e) {  // 2^e, -126 <= e <= 127
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Range [start, end) of the block's units and the sequence that holds the
+// first one.  units(b) gives a sequence's units.  All threads of the block
+// (kThreads of them) call it and get the same values.
+struct Range {
+    int64_t total, start, end;
+    int blocks;   // blocks that have units: the first min(gridDim.x, total)
+    int b;
+    int64_t off;  // of `start` within sequence b's units
+};
+struct RangeSmem {
+    int64_t warp[33];
+    int64_t off;
+    int b;
+};
+
+template <int kThreads, class Units>
+__device__ __forceinline__ Range block_range(int n_seq, RangeSmem *sm, Units units) {
+    constexpr int kWarps = kThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Range r;
+    int64_t sum = 0, v = 0;
+    for (int i = threadIdx.x; i < n_seq; i += kThreads) sum += v = units(i);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sm->warp[warp] = sum;
+    __syncthreads();
+    r.total = 0;
+    for (int w = 0; w < kWarps; ++w) r.total += sm->warp[w];
+    r.b = 0;
+    r.off = r.start = r.end = 0;
+    r.blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), r.total));
+    if (static_cast<int>(blockIdx.x) >= r.blocks) return r;
+    r.start = r.total * blockIdx.x / r.blocks;
+    r.end = r.total * (blockIdx.x + 1) / r.blocks;
+    int64_t before = 0;
+    for (int base = 0; base < n_seq; base += kThreads) {
+        const int i = base + threadIdx.x;
+        if (n_seq > kThreads) v = i < n_seq ? units(i) : 0;
+        int64_t inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        __syncthreads();
+        if (lane == 31) sm->warp[warp] = inc;
+        __syncthreads();
+        int64_t p = before + inc - v;  // units before sequence i
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) p += sm->warp[w];
+            before += sm->warp[w];
+        }
+        if (p <= r.start && r.start < p + v) {
+            sm->b = i;
+            sm->off = r.start - p;
+        }
+        if (before > r.start) break;  // the same in every thread
+    }
+    __syncthreads();
+    r.b = sm->b;
+    r.off = sm->off;
+    return r;
+}
+
+// The block whose range holds unit u.
+__device__ __forceinline__ int block_of_unit(int64_t u, const Range &r) {
+    return static_cast<int>(((u + 1) * r.blocks - 1) / r.total);
+}
+
+// A partial result: maxima and sums (base 2) and the normalized output of
+// `rows` rows: [rows] + [rows] + [rows][dim] floats.
+__host__ __device__ constexpr int64_t slot_floats(int rows, int dim) {
+    return int64_t(rows) * (dim + 2);
+}
+
+inline uint32_t page_magic(int page) {
+    const uint32_t d = static_cast<uint32_t>(page) >> 4;
+    return d == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((uint64_t(1) << 32) / d);
+}
+
+// Joins the partial results of items that several blocks share; after each
+// attention kernel, with that kernel's grid and `tile` rows per slot.
+int launch_combine(const Attn &a, int grid, int tile, int dim, int xt, cudaStream_t stream);
+
+// Items of up to 16 (row, head) pairs: warp-level MMA (w4kv_attn_rows.cu).
+int launch_rows_attention(const Attn &a, int fmt, int dim, int xt, int tile, int grid,
+                          cudaStream_t stream);
+
+}  // namespace kv
+}  // namespace w4

@@ -1,0 +1,706 @@
+// w4kv_attn_rows.cu -- attention of few rows over the quantized cache: decode
+// steps and short proposals, up to 16 (row, query head) pairs per key/value
+// head.
+//
+// Mathematics: one pass over the cache with a running maximum m, sum l and
+// output O per row; a score is q . codes times the key row's scale, a weight
+// is p = 2^(score - m) times the value row's scale.  The codes enter the MMAs
+// exactly (INT8 and E4M3 are fp16 numbers, and so are an INT4 value's u - z and
+// 16 (u - z); an INT4 key enters as the fp16 subnormals u * 2^-24, with
+// q . (u - z) = q . u - z sum q.  For the values that form is too coarse: the
+// MMA aligns a subnormal as if it were 2^-14, which leaves an error of 2^-14 of
+// the largest weight where u - z is 0).  m moves only when a score exceeds it by
+// 2^8, so that O is rarely rescaled; p <= 2^8 then, and the value scales are
+// taken relative to 2^k > their running maximum / 2^7, so that a weight fits
+// fp16 (below 2^15) with 21 bits of range under the largest one.
+//
+// HBM bounds it: a token of a head is 2 (dim + 4) bytes (INT8) and a few
+// thousand multiplications.  The layout keeps the shared-memory and register
+// work off that path:
+//   * S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16, cached tokens (or
+//     dims) as the 16 rows and query rows as the 8 columns: a decode step of
+//     8 heads per key/value head fills the tile; tcgen05's 128 rows would be
+//     15/16 padding.
+//   * every lane copies (cp.async) exactly the code bytes of its own fragments
+//     into its own slots of the warp's ring: contiguous pieces of a row, no
+//     exchange between lanes, no bank conflicts.  Which dim a fragment index
+//     stands for is free (the contraction index of S, the row index of O^T),
+//     so a lane's piece of a row becomes consecutive fragments.
+//   * value fragments pair two tokens of one dim: bytes of two rows'
+//     words, merged with byte permutations.
+//   * P^T needs one 8x8 transpose per 8 tokens (movmatrix).
+// A block of 8 warps takes an item's 16-token tiles round robin (two at a
+// time per warp, for two independent MMA chains), joins its warps' results in
+// shared memory at the item's end, and prefetches across items.
+
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "w4kv_attn.cuh"
+
+namespace w4 {
+namespace kv {
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kTile = 16;  // tokens per MMA tile
+
+template <int FMT, int D, int NT>
+struct Shape {
+    static constexpr int kRow = FMT == W4KV_INT4 ? D / 2 : D;  // code bytes of a row
+    static constexpr int kKB = kRow / 4, kVB = kRow / 8;       // a lane's bytes of a key / value row
+    static constexpr int kStage = 2 * kTile * kRow + 128;      // codes, then 32 scale words
+    static constexpr int kStages = kRow == 128 ? 6 : 8;
+    static constexpr int kSteps = D / 16;  // k steps of S, row tiles of O^T
+    static constexpr int kTileRows = 8 * NT;
+    static constexpr int kPhase = 64 / NT < D ? 64 / NT : D;  // dims joined at a time
+    static constexpr int kPad = kPhase + 8;
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kJoin = kWarps * kTileRows * kPad * 4;
+    static constexpr int kStats = kWarps * kTileRows * 2 * 4;
+    static constexpr int kSmem = kRing + kJoin + kStats + static_cast<int>(sizeof(RangeSmem)) + 16;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Copies N bytes, or writes N zeros.
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool live) {
+    const int n = live ? N : 0;
+    if (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else if (N == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    return __byte_perm(a, b, sel);
+}
+
+// Four code bytes -> two fp16 pairs (bytes 0, 1 and 2, 3).
+template <int FMT>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t *lo, uint32_t *hi) {
+    if (FMT == W4KV_INT8) {  // 1152 + q as fp16 bits 0x64(q ^ 0x80), then - 1152
+        const uint32_t x = w ^ 0x80808080u;
+        const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+        const uint32_t l = prmt(x, 0x64646464u, 0x4140), h = prmt(x, 0x64646464u, 0x4342);
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&l), bias);
+        const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&h), bias);
+        *lo = *reinterpret_cast<const uint32_t *>(&a);
+        *hi = *reinterpret_cast<const uint32_t *>(&b);
+    } else {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(*lo), "=r"(*hi)
+            : "r"(w));
+    }
+}
+
+// The dims of k step s of lane c: fragment k 2c, 2c + 1 are d, d + 1 and
+// k 2c + 8, 2c + 9 are d + 2, d + 3.
+template <int FMT, int D>
+__device__ __forceinline__ int key_dim(int c, int s) {
+    constexpr int kKB = (FMT == W4KV_INT4 ? D / 2 : D) / 4;
+    if (FMT == W4KV_INT4) return 2 * (c * kKB + 4 * (s >> 1)) + 4 * (s & 1);
+    if (kKB == 32) return 16 * (c + 4 * (s >> 2)) + 4 * (s & 3);  // two 16-byte pieces, 64 apart
+    return c * kKB + 4 * s;
+}
+
+// Where a walk over the block's units stands: an item and its tiles.
+struct Walk {
+    Seq s;
+    int b, h;         // sequence, key/value head
+    int u, nu;        // next unit of the item, units of the item
+    int64_t rem;      // units of the block not yet walked
+    int take;         // units of the current segment (the item's part in the block's range)
+    int tile, end;    // its tiles: this warp's next one, the first behind it
+};
+
+template <int FMT, int D, int XT, int NT>
+__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
+    using S = Shape<FMT, D, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    uint8_t *ring = smem + warp * S::kStages * S::kStage;
+    const uint32_t ring_u = smem_u32(ring);
+    float *join = reinterpret_cast<float *>(smem + S::kRing);
+    float *stat_m = reinterpret_cast<float *>(smem + S::kRing + S::kJoin);  // [warps][rows]
+    float *stat_l = stat_m + kWarps * S::kTileRows;
+    RangeSmem *rsm = reinterpret_cast<RangeSmem *>(
+        smem + ((S::kRing + S::kJoin + S::kStats + 15) & ~15));
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    auto item_units = [](const Seq &s) {
+        return max(1, ((s.hi + 15) / 16 - s.lo / 16 + kUnit / 16 - 1) / (kUnit / 16));
+    };
+    const Range range = block_range<kThreads>(a.b.n, rsm, [&](int b) -> int64_t {
+        const Seq s = load_seq(a, b);
+        return s.n > 0 ? int64_t(item_units(s)) * a.c.heads : 0;
+    });
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (range.start == range.end) return;
+
+    // Opens the segment (the part of one item in this block's range) at w.b, w.h, w.u.
+    auto open = [&](Walk &w) {
+        const int t0 = w.s.lo / 16 + w.u * (kUnit / 16);
+        w.take = static_cast<int>(min(static_cast<int64_t>(w.nu - w.u), w.rem));
+        w.tile = t0 + warp;
+        w.end = min((w.s.hi + 15) / 16, t0 + w.take * (kUnit / 16));
+        w.rem -= w.take;
+        w.u += w.take;
+    };
+    auto next_item = [&](Walk &w) {  // only while w.rem > 0: a later item exists
+        w.u = 0;
+        if (++w.h == a.c.heads) {
+            w.h = 0;
+            do {
+                if (w.b + 1 < a.b.n) ++w.b;
+                w.s = load_seq(a, w.b);
+            } while (w.s.n == 0 && w.b + 1 < a.b.n);
+            w.nu = item_units(w.s);
+        }
+    };
+    Walk w;
+    w.b = range.b;
+    w.s = load_seq(a, w.b);
+    w.nu = item_units(w.s);
+    w.h = static_cast<int>(range.off / w.nu);
+    w.u = static_cast<int>(range.off % w.nu);
+    w.rem = range.end - range.start;
+    open(w);
+    Walk p = w;  // the producer's walk, ahead of the consumer's
+
+    // ---- producer: fragment bytes of one tile per stage ----
+    int p_id = 0, p_rest = 0, issued = 0;
+    bool p_live = true;  // a tile is left to issue
+    auto fetch_page = [&]() {
+        while (p.tile >= p.end) {  // to the next segment that has a tile for this warp
+            if (p.rem == 0) {
+                p_live = false;
+                return;
+            }
+            next_item(p);
+            open(p);
+        }
+        const int pg = page_of_tile(a, p.tile, &p_rest);
+        p_id = pg < a.b.width ? __ldg(a.b.table + p.b * a.b.stride + pg) : -1;
+    };
+    fetch_page();
+    uint32_t bad_mask = 0;  // per stage: the tile's page number was out of range
+    auto issue = [&]() {
+        if (p_live) {
+            const int slot = issued % S::kStages;
+            const uint32_t dst = ring_u + slot * S::kStage;
+            const bool ok = p_id >= 0 && p_id < a.c.pages;
+            if (!ok && lane == 0) atomicOr(a.status, kStatusBounds);
+            bad_mask = ok ? bad_mask & ~(1u << slot) : bad_mask | (1u << slot);
+            const int64_t r0 = ok ? (int64_t(p_id) * a.c.heads + p.h) * a.c.page + p_rest * kTile : 0;
+            const int kv0 = p.tile * kTile;
+            const int v0 = ok ? max(0, p.s.lo - kv0) : kTile, v1 = p.s.hi - kv0;  // rows in use
+            const uint8_t *kp = a.c.k + r0 * S::kRow, *vp = a.c.v + r0 * S::kRow;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // key rows g, g + 8
+                const int r = g + 8 * i;
+                const bool live = r >= v0 && r < v1;
+                if (S::kKB == 32) {
+                    copy_async<16>(dst + (2 * i) * 512 + lane * 16, kp + r * S::kRow + c * 16, live);
+                    copy_async<16>(dst + (2 * i + 1) * 512 + lane * 16, kp + r * S::kRow + 64 + c * 16, live);
+                } else if (S::kKB == 16) {
+                    copy_async<16>(dst + i * 512 + lane * 16, kp + r * S::kRow + c * 16, live);
+                } else {
+                    copy_async<8>(dst + i * 256 + lane * 8, kp + r * S::kRow + c * 8, live);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // value rows 2c, 2c + 1, 2c + 8, 2c + 9
+                const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+                copy_async<S::kVB>(dst + kTile * S::kRow + (i * 32 + lane) * S::kVB,
+                                   vp + r * S::kRow + g * S::kVB, r >= v0 && r < v1);
+            }
+            {  // scale words: 16 of the keys, 16 of the values
+                const int r = lane & 15;
+                copy_async<4>(dst + 2 * kTile * S::kRow + lane * 4,
+                              (lane < 16 ? a.c.ks : a.c.vs) + r0 + r, r >= v0 && r < v1);
+            }
+            p.tile += kWarps;
+            fetch_page();
+        }
+        ++issued;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) issue();
+    int consumed = 0;
+
+    while (true) {  // segments
+        // ---- the item's query rows as B fragments, and what each column sees ----
+        uint32_t bq[NT][S::kSteps][2];
+        float f1[NT][2], f2[NT][2], qsum[NT][2];
+        int clo[NT][2], chi[NT][2];
+        const int R = w.s.n * a.group;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g;
+            const bool live = r < R;
+            const int i = r / a.group;
+            const uint16_t *qp = a.q + int64_t(w.s.row0 + i) * a.q_row +
+                                 (w.h * a.group + r - i * a.group) * a.q_head;
+            uint2 raw[S::kSteps];
+            uint32_t top = 0;
+#pragma unroll
+            for (int s = 0; s < S::kSteps; ++s) {
+                raw[s] = live ? __ldg(reinterpret_cast<const uint2 *>(qp + key_dim<FMT, D>(c, s)))
+                              : make_uint2(0, 0);
+                const uint32_t x = raw[s].x & 0x7FFF7FFFu, y = raw[s].y & 0x7FFF7FFFu;
+                const uint32_t z = __vmaxu2(x, y);
+                top = max(top, max(z & 0xFFFFu, z >> 16));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the row times 2^sh has its largest element in [2^10, 2^11)
+            int sh = 0;
+            {
+                const uint32_t t32 = __float_as_uint(widen1<XT>(static_cast<uint16_t>(top)));
+                if (t32 != 0 && t32 < 0x7F800000u) sh = min(120, 137 - static_cast<int>(t32 >> 23));
+            }
+            const float up = pow2i(sh);
+            float sum = 0.f;
+#pragma unroll
+            for (int s = 0; s < S::kSteps; ++s) {
+                const float e0 = widen1<XT>(raw[s].x & 0xFFFF) * up, e1 = widen1<XT>(raw[s].x >> 16) * up;
+                float e2 = widen1<XT>(raw[s].y & 0xFFFF) * up, e3 = widen1<XT>(raw[s].y >> 16) * up;
+                if (FMT == W4KV_INT4) {  // the second pair's codes stand 4 bits higher
+                    e2 *= 0.0625f;
+                    e3 *= 0.0625f;
+                }
+                const __half2 h0 = __floats2half2_rn(e0, e1), h1 = __floats2half2_rn(e2, e3);
+                if (FMT == W4KV_INT4) {
+                    const float2 x = __half22float2(h0), y = __half22float2(h1);
+                    sum += (x.x + x.y) + 16.f * (y.x + y.y);
+                }
+                bq[nt][s][0] = *reinterpret_cast<const uint32_t *>(&h0);
+                bq[nt][s][1] = *reinterpret_cast<const uint32_t *>(&h1);
+            }
+            if (FMT == W4KV_INT4) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            }
+            // this lane's score columns are 2c, 2c + 1: their rows' values live in lanes 8c, 8c + 4
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int s2 = __shfl_sync(0xffffffffu, sh, 8 * c + 4 * e);
+                qsum[nt][e] = FMT == W4KV_INT4 ? __shfl_sync(0xffffffffu, sum, 8 * c + 4 * e) : 0.f;
+                f1[nt][e] = pow2i(-(s2 / 2));
+                f2[nt][e] = pow2i(-(s2 - s2 / 2)) * a.scale_log2;
+                const int rr = nt * 8 + 2 * c + e;
+                const int pos = w.s.first + rr / a.group;
+                clo[nt][e] = w.s.lo;
+                chi[nt][e] = w.s.hi;
+                if (a.causal && rr < R) {
+                    chi[nt][e] = min(w.s.hi, pos + 1);
+                    if (a.window > 0) clo[nt][e] = max(w.s.lo, pos + 1 - a.window);
+                }
+            }
+        }
+        // tiles inside [all_lo, all_hi) are seen whole by every row
+        const int all_hi = a.causal ? min(w.s.hi, w.s.first + 1) : w.s.hi;
+        const int all_lo = a.window > 0 ? max(w.s.lo, w.s.first + w.s.n - a.window) : w.s.lo;
+
+        float m[NT][2], l[NT][2], o[NT][S::kSteps][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[nt][e] = -INFINITY;
+                l[nt][e] = 0.f;
+            }
+#pragma unroll
+            for (int t = 0; t < S::kSteps; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nt][t][i] = 0.f;
+        }
+        int vexp = 0;  // exponent field of the largest value scale so far: a weight is p * scale * 2^(133 - vexp)
+
+        auto consume = [&](auto np_tag) {
+            constexpr int NP = decltype(np_tag)::value;
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - NP) : "memory");
+            __syncwarp();
+            uint32_t kw[NP][2][S::kKB / 4], vw[NP][4][S::kVB / 4], ksw[NP][2], vsw[NP][2];
+            uint32_t vz[NP][2];  // zero points of the value rows 2c, 2c + 1 and 2c + 8, 2c + 9
+            bool bad[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const int slot = (consumed + n) % S::kStages;
+                const uint8_t *st = ring + slot * S::kStage;
+                bad[n] = (bad_mask >> slot) & 1;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (S::kKB >= 16) {
+#pragma unroll
+                        for (int j = 0; j < S::kKB / 16; ++j) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(
+                                st + (i * (S::kKB / 16) + j) * 512 + lane * 16);
+                            kw[n][i][4 * j] = v.x, kw[n][i][4 * j + 1] = v.y;
+                            kw[n][i][4 * j + 2] = v.z, kw[n][i][4 * j + 3] = v.w;
+                        }
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(st + i * 256 + lane * 8);
+                        kw[n][i][0] = v.x, kw[n][i][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t *vp = st + kTile * S::kRow + (i * 32 + lane) * S::kVB;
+                    if (S::kVB == 16) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(vp);
+                        vw[n][i][0] = v.x, vw[n][i][1] = v.y, vw[n][i][2] = v.z, vw[n][i][3] = v.w;
+                    } else if (S::kVB == 8) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(vp);
+                        vw[n][i][0] = v.x, vw[n][i][1] = v.y;
+                    } else {
+                        vw[n][i][0] = *reinterpret_cast<const uint32_t *>(vp);
+                    }
+                }
+                const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + 2 * kTile * S::kRow);
+                ksw[n][0] = sw[g], ksw[n][1] = sw[g + 8];
+                vsw[n][0] = sw[16 + g], vsw[n][1] = sw[24 + g];
+                if (FMT == W4KV_INT4) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint2 z = *reinterpret_cast<const uint2 *>(sw + 16 + 2 * c + 8 * q);
+                        vz[n][q] = (z.x & 15u) | (z.y & 15u) << 16;
+                    }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < NP; ++n) issue();
+            // ---- S^T = K Q^T ----
+            float sc[NP][NT][4];
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[n][nt][i] = 0.f;
+#pragma unroll
+            for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    uint32_t fa[4];
+                    if (FMT == W4KV_INT4) {  // nibbles as subnormals u * 2^-24, or 16 u * 2^-24
+                        const uint32_t x = kw[n][0][s >> 1] >> (8 * (s & 1));
+                        const uint32_t y = kw[n][1][s >> 1] >> (8 * (s & 1));
+                        fa[0] = x & 0x000F000Fu, fa[2] = x & 0x00F000F0u;
+                        fa[1] = y & 0x000F000Fu, fa[3] = y & 0x00F000F0u;
+                    } else {
+                        widen4<FMT>(kw[n][0][s], &fa[0], &fa[2]);
+                        widen4<FMT>(kw[n][1][s], &fa[1], &fa[3]);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma(sc[n][nt], fa, bq[nt][s][0], bq[nt][s][1]);
+                }
+            // ---- scores in base 2, masked ----
+            bool grow = false;
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const int kv0 = (w.tile + n * kWarps) * kTile;
+                const bool cut = bad[n] || kv0 < all_lo || kv0 + kTile > all_hi;  // warp-uniform
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int e = i & 1, kw_ = ksw[n][i >> 1];
+                        float x = sc[n][nt][i];
+                        if (FMT == W4KV_INT4) x = fmaf(x, 16777216.f, -static_cast<float>(kw_ & 15) * qsum[nt][e]);
+                        const float ks = FMT == W4KV_INT4 ? int4_scale(kw_) : __uint_as_float(kw_);
+                        x = x * f1[nt][e] * ks * f2[nt][e];
+                        if (cut) {
+                            const int j = kv0 + g + 8 * (i >> 1);
+                            if (bad[n] || j < clo[nt][e] || j >= chi[nt][e]) x = -INFINITY;
+                        }
+                        sc[n][nt][i] = x;
+                        grow = grow || x > m[nt][e] + 8.f;
+                    }
+            }
+            // ---- new reference maxima and value exponent, if they moved ----
+            uint32_t ve = 0;
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t e = (vsw[n][i] >> 23) & 255u;
+                    ve = max(ve, e == 255u ? 0u : e);
+                }
+            ve = __reduce_max_sync(0xffffffffu, ve);
+            const bool vgrow = static_cast<int>(ve) > vexp;
+            if (__any_sync(0xffffffffu, grow) || vgrow) {
+                float fv = 1.f;
+                if (vgrow) {  // below 7 the multiplier stays at 2^126
+                    fv = pow2i(max(-126, max(vexp, 7) - max(static_cast<int>(ve), 7)));
+                    vexp = static_cast<int>(ve);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = m[nt][e];
+#pragma unroll
+                        for (int n = 0; n < NP; ++n) x = fmaxf(x, fmaxf(sc[n][nt][e], sc[n][nt][e + 2]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        f[e] = m[nt][e] == -INFINITY ? 1.f : ex2(m[nt][e] - x);
+                        m[nt][e] = x;
+                        l[nt][e] *= f[e];
+                        f[e] *= fv;
+                    }
+#pragma unroll
+                    for (int t = 0; t < S::kSteps; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[nt][t][i] *= f[i & 1];
+                }
+            }
+            const float vmul = pow2i(133 - max(vexp, 7));
+            // ---- weights, transposed into B fragments ----
+            uint32_t pb[NP][NT][2];
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // tokens g, g + 8
+                    const uint32_t vw_ = vsw[n][i];
+                    const float vs = (FMT == W4KV_INT4 ? int4_scale(vw_) : __uint_as_float(vw_)) * vmul;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float pw[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = sc[n][nt][2 * i + e];
+                            const float pe = ex2(x - (m[nt][e] == -INFINITY ? 0.f : m[nt][e]));
+                            l[nt][e] += pe;
+                            // unseen: exactly zero, whatever the value row's scale is
+                            pw[e] = x == -INFINITY ? 0.f : pe * vs;
+                        }
+                        const __half2 h = __floats2half2_rn(pw[0], pw[1]);
+                        pb[n][nt][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
+                    }
+                }
+            // ---- O^T += V^T P^T ----
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                if (FMT == W4KV_INT4) {
+#pragma unroll
+                    for (int j = 0; j < S::kVB / 4; ++j) {
+                        uint32_t x[2][2];  // [low, high nibbles' halves][tokens 2c.., 2c + 8..]
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            x[0][q] = prmt(vw[n][2 * q][j], vw[n][2 * q + 1][j], 0x5410);
+                            x[1][q] = prmt(vw[n][2 * q][j], vw[n][2 * q + 1][j], 0x7632);
+                        }
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {  // dims 8j + 2t, 8j + 2t + 1; 16-fold for odd t
+                            // 1024 + u as fp16 bits 0x6400 | u (or 16 u), then - (1024 + z)
+                            const uint32_t mask = t & 1 ? 0x00F000F0u : 0x000F000Fu;
+                            const int sh = t & 2 ? 8 : 0;
+                            uint32_t fa[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t u = ((x[q & 1][q >> 1] >> sh) & mask) | 0x64006400u;
+                                const uint32_t z = (vz[n][q >> 1] << (t & 1 ? 4 : 0)) | 0x64006400u;
+                                const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u),
+                                                          *reinterpret_cast<const __half2 *>(&z));
+                                fa[q] = *reinterpret_cast<const uint32_t *>(&r);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma(o[nt][4 * j + t], fa, pb[n][nt][0], pb[n][nt][1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < S::kVB / 4; ++j) {
+                        uint32_t fa[2][4];  // dims 4j, 4j + 1 and 4j + 2, 4j + 3
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t x = prmt(vw[n][2 * q][j], vw[n][2 * q + 1][j], 0x5140);
+                            const uint32_t y = prmt(vw[n][2 * q][j], vw[n][2 * q + 1][j], 0x7362);
+                            widen4<FMT>(x, &fa[0][2 * q], &fa[0][2 * q + 1]);
+                            widen4<FMT>(y, &fa[1][2 * q], &fa[1][2 * q + 1]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma(o[nt][2 * j + t], fa[t], pb[n][nt][0], pb[n][nt][1]);
+                    }
+                }
+            }
+            consumed += NP;
+            w.tile += NP * kWarps;
+        };
+        while (w.tile + kWarps < w.end) consume(std::integral_constant<int, 2>());
+        if (w.tile < w.end) consume(std::integral_constant<int, 1>());
+
+        // ---- the warps' results together ----
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+                }
+                if (g == 0) {
+                    const int r = warp * S::kTileRows + nt * 8 + 2 * c + e;
+                    stat_m[r] = m[nt][e];
+                    stat_l[r] = l[nt][e];
+                }
+            }
+        __syncthreads();
+        const float vback = pow2i(max(vexp, 7) - 133);  // 1 / vmul
+        float wgt[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = nt * 8 + 2 * c + e;
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q) M = fmaxf(M, stat_m[q * S::kTileRows + r]);
+                const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q)
+                    L += stat_l[q * S::kTileRows + r] * ex2(stat_m[q * S::kTileRows + r] - mu);
+                wgt[nt][e] = L == 0.f ? 0.f : ex2(m[nt][e] - mu) / L;
+            }
+        // where the item's units lie among the blocks
+        const bool from_start = w.u == w.take;
+        const bool to_end = w.u == w.nu;
+        const bool whole = from_start && to_end;
+        float *slot = a.slots + (2 * int64_t(blockIdx.x) + (from_start ? 1 : 0)) *
+                                    slot_floats(S::kTileRows, D);
+        if (!whole && from_start && threadIdx.x == 0) {
+            const int64_t last = range.end - w.rem + (w.nu - w.u) - 1;
+            a.desc[blockIdx.x] =
+                make_int4(w.b, w.h, block_of_unit(last, range) - static_cast<int>(blockIdx.x) + 1, 0);
+        }
+        if (threadIdx.x < S::kTileRows) {
+            const int r = threadIdx.x;
+            float M = -INFINITY, L = 0.f;
+            for (int q = 0; q < kWarps; ++q) M = fmaxf(M, stat_m[q * S::kTileRows + r]);
+            const float mu = M == -INFINITY ? 0.f : M;
+            for (int q = 0; q < kWarps; ++q)
+                L += stat_l[q * S::kTileRows + r] * ex2(stat_m[q * S::kTileRows + r] - mu);
+            if (!whole) {
+                slot[r] = M;
+                slot[S::kTileRows + r] = L;
+            } else if (a.lse && r < R) {
+                const int i = r / a.group;
+                a.lse[int64_t(w.s.row0 + i) * a.heads + w.h * a.group + r - i * a.group] =
+                    L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            }
+        }
+#pragma unroll
+        for (int ph = 0; ph < D / S::kPhase; ++ph) {
+            constexpr int kT = S::kPhase / 16;  // row tiles of O^T per phase
+            if (ph) __syncthreads();            // the previous phase has been read
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int t = 0; t < kT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = o[nt][ph * kT + t][e], y = o[nt][ph * kT + t][e + 2];
+                        if (FMT == W4KV_INT4 && ((ph * kT + t) & 1)) {  // 16-fold codes
+                            x *= 0.0625f;
+                            y *= 0.0625f;
+                        }
+                        *reinterpret_cast<float2 *>(
+                            join + (warp * S::kTileRows + nt * 8 + 2 * c + e) * S::kPad + t * 16 + 2 * g) =
+                            make_float2(x * wgt[nt][e] * vback, y * wgt[nt][e] * vback);
+                    }
+            __syncthreads();
+            for (int i = threadIdx.x; i < S::kTileRows * S::kPhase / 2; i += kThreads) {
+                const int r = i / (S::kPhase / 2), j = i - r * (S::kPhase / 2);
+                if (r >= R) break;
+                float x = 0.f, y = 0.f;
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q) {
+                    const float2 v = *reinterpret_cast<const float2 *>(
+                        join + (q * S::kTileRows + r) * S::kPad + 2 * j);
+                    x += v.x;
+                    y += v.y;
+                }
+                const int d = (D / 8) * (j & 7) + 2 * (ph * kT + (j >> 3));
+                if (whole) {
+                    const int t = r / a.group;
+                    *reinterpret_cast<uint32_t *>(a.o + int64_t(w.s.row0 + t) * a.o_row +
+                                                  (w.h * a.group + r - t * a.group) * a.o_head + d) =
+                        narrow1<XT>(x) | static_cast<uint32_t>(narrow1<XT>(y)) << 16;
+                } else {
+                    *reinterpret_cast<float2 *>(slot + 2 * S::kTileRows + r * D + d) = make_float2(x, y);
+                }
+            }
+        }
+        if (w.rem == 0) break;
+        next_item(w);
+        open(w);
+        __syncthreads();  // join and the statistics are read before they are written again
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <int FMT, int D, int XT, int NT>
+int run(const Attn &a, int grid, cudaStream_t stream) {
+    using S = Shape<FMT, D, NT>;
+    auto kernel = rows_kernel<FMT, D, XT, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(rows_kernel)", e);
+    kernel<<<grid, kThreads, S::kSmem, stream>>>(a);
+    return cuda_status(cudaGetLastError());
+}
+
+template <int FMT, int D>
+int run_x(const Attn &a, int xt, int tile, int grid, cudaStream_t s) {
+    if (xt == W4_F16)
+        return tile == 8 ? run<FMT, D, W4_F16, 1>(a, grid, s) : run<FMT, D, W4_F16, 2>(a, grid, s);
+    return tile == 8 ? run<FMT, D, W4_BF16, 1>(a, grid, s) : run<FMT, D, W4_BF16, 2>(a, grid, s);
+}
+
+}  // namespace
+
+int launch_rows_attention(const Attn &a, int fmt, int dim, int xt, int tile, int grid,
+                          cudaStream_t stream) {
+    if (dim == 64) {
+        if (fmt == W4KV_INT8) return run_x<W4KV_INT8, 64>(a, xt, tile, grid, stream);
+        if (fmt == W4KV_E4M3) return run_x<W4KV_E4M3, 64>(a, xt, tile, grid, stream);
+        return run_x<W4KV_INT4, 64>(a, xt, tile, grid, stream);
+    }
+    if (fmt == W4KV_INT8) return run_x<W4KV_INT8, 128>(a, xt, tile, grid, stream);
+    if (fmt == W4KV_E4M3) return run_x<W4KV_E4M3, 128>(a, xt, tile, grid, stream);
+    return run_x<W4KV_INT4, 128>(a, xt, tile, grid, stream);
+}
+
+}  // namespace kv
+}  // namespace w4
