@@ -118,13 +118,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const Attn a, int tile, in
         const int r = i / (dim / 4), e = (i - r * (dim / 4)) * 4;
         float M = first[r];
         for (int q = 1; q < d.z; ++q) M = fmaxf(M, rest[2 * q * slot + r]);
-        const float mu = M == -INFINITY ? 0.f : M;
         float L = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int q = 0; q < d.z; ++q) {
             const float *p = q ? rest + 2 * q * slot : first;
-            const float w = p[tile + r] * ex2(p[r] - mu);
+            const float w = p[tile + r] * ex2(p[r] - M);
             const float4 v = *reinterpret_cast<const float4 *>(p + 2 * tile + r * dim + e);
             L += w;
             o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
@@ -176,7 +175,7 @@ Plan make_plan(const DeviceInfo &d, int dim, int64_t batch, int64_t max_rows, in
     p.tiled = pairs > 16;
     if (pairs <= 8) p.rows_tile = 8;
     else if (pairs <= 16 || (batch > 1 && group <= 16)) p.rows_tile = 16;
-    p.grid = d.sm_count;
+    p.grid = (p.rows_tile == 8 ? 4 : 3) * d.sm_count;
     const size_t desc = (size_t(p.grid) * 16 + 255) & ~size_t(255);
     p.slots = 2 * size_t(p.grid) * slot_floats(p.rows_tile, dim) * 4;
     p.total = p.rows_tile ? desc + ((p.slots + 255) & ~size_t(255)) : 0;

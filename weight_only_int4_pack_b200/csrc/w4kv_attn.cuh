@@ -3,9 +3,11 @@
 // thread blocks, and the layout of the partial results.
 //
 // Work is counted in units of 128 cached tokens of an item (a key/value head
-// of a sequence; in the tiled kernel, of a tile of its rows).  The units of
-// all items, in the order (sequence, tile, head), are cut into gridDim.x equal
-// ranges; an item that a cut divides is finished by combine_kernel from the
+// of a sequence; in the tiled kernel, of a tile of its rows), plus kItemCost
+// per item for its queries and its output: positions kItemCost + u for unit u,
+// the first unit standing for the positions before it too.  The positions of
+// all items, in the order (sequence, tile, head), are cut into equal ranges, one
+// per block; an item that a cut divides is finished by combine_kernel from the
 // partial results of its blocks, in block order (deterministic).  The lengths
 // live on the device, so every block finds its range itself: a block-wide sum
 // over the sequences, then a scan of the 256 that hold its first unit.
@@ -16,7 +18,8 @@
 namespace w4 {
 namespace kv {
 
-constexpr int kUnit = 128;  // cached tokens per unit of work
+constexpr int kUnit = 128;    // cached tokens per unit of work
+constexpr int kItemCost = 4;  // what an item costs beside its units, in units
 
 struct Attn {
     Cache c;
@@ -98,14 +101,14 @@ __device__ __forceinline__ float pow2i(int e) {  // 2^e, -126 <= e <= 127
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Range [start, end) of the block's units and the sequence that holds the
-// first one.  units(b) gives a sequence's units.  All threads of the block
+// Range [start, end) of the block in the cost of all items, and the sequence that holds its
+// beginning.  units(b) gives the cost of a sequence's items.  All threads of the block
 // (kThreads of them) call it and get the same values.
 struct Range {
     int64_t total, start, end;
     int blocks;   // blocks that have units: the first min(gridDim.x, total)
     int b;
-    int64_t off;  // of `start` within sequence b's units
+    int64_t off;  // of `start` within sequence b
 };
 struct RangeSmem {
     int64_t warp[33];
@@ -166,6 +169,10 @@ __device__ __forceinline__ Range block_range(int n_seq, RangeSmem *sm, Units uni
 __device__ __forceinline__ int block_of_unit(int64_t u, const Range &r) {
     return static_cast<int>(((u + 1) * r.blocks - 1) / r.total);
 }
+
+// Reference maximum of a row that has seen nothing: below every score, and
+// finite, so that differences of maxima are numbers.
+constexpr float kNone = -1e30f;
 
 // A partial result: maxima and sums (base 2) and the normalized output of
 // `rows` rows: [rows] + [rows] + [rows][dim] floats.

@@ -44,7 +44,7 @@ namespace w4 {
 namespace kv {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // tokens per MMA tile
 
 template <int FMT, int D, int NT>
@@ -52,10 +52,12 @@ struct Shape {
     static constexpr int kRow = FMT == W4KV_INT4 ? D / 2 : D;  // code bytes of a row
     static constexpr int kKB = kRow / 4, kVB = kRow / 8;       // a lane's bytes of a key / value row
     static constexpr int kStage = 2 * kTile * kRow + 128;      // codes, then 32 scale words
-    static constexpr int kStages = kRow == 128 ? 6 : 8;
+    static constexpr int kBlocks = NT == 1 ? 4 : 3;  // blocks per SM
+    static constexpr int kAtOnce = 1;                // tiles that a warp takes at a time
+    static constexpr int kStages = kRow == 128 ? 3 : 6;
     static constexpr int kSteps = D / 16;  // k steps of S, row tiles of O^T
     static constexpr int kTileRows = 8 * NT;
-    static constexpr int kPhase = 64 / NT < D ? 64 / NT : D;  // dims joined at a time
+    static constexpr int kPhase = 32;  // dims joined at a time
     static constexpr int kPad = kPhase + 8;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kJoin = kWarps * kTileRows * kPad * 4;
@@ -67,16 +69,49 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Copies N bytes, or writes N zeros.
-template <int N>
+// Copies N bytes; with kCut, or writes N zeros.
+template <int N, bool kCut>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool live) {
     const int n = live ? N : 0;
-    if (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else if (N == 8)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    if (N == 16) {
+        if (kCut)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+        else
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    } else if (kCut) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(N) : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+    }
+}
+
+// A tile's fragment bytes and scale words into a stage: the lane's pieces of
+// key rows g, g + 8, of value rows 2c, 2c + 1, 2c + 8, 2c + 9, and scale word
+// `lane` (16 of the keys, 16 of the values).  kp, vp, sp point to the lane's
+// first piece; dst counts the lane in already for 16-byte pieces.  With kCut
+// only rows [v0, v1) are read, the others are zeros.
+template <class S, bool kCut>
+__device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t *kp, const uint8_t *vp,
+                                          const float *sp, int lane, int v0, int v1) {
+    const int g = lane >> 2, c = lane & 3;
+    constexpr int kP = S::kKB < 16 ? S::kKB : 16;  // bytes of a key piece
+    const uint32_t kd = stage + lane * kP, vd = stage + kTile * S::kRow + lane * S::kVB;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool live = !kCut || (g + 8 * i >= v0 && g + 8 * i < v1);
+#pragma unroll
+        for (int j = 0; j < S::kKB / kP; ++j)
+            copy_async<kP, kCut>(kd + (i * (S::kKB / kP) + j) * 32 * kP,
+                                 kp + 8 * i * S::kRow + j * 64, live);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (i & 1) + 8 * (i >> 1);
+        copy_async<S::kVB, kCut>(vd + i * 32 * S::kVB, vp + r * S::kRow,
+                                 !kCut || (2 * c + r >= v0 && 2 * c + r < v1));
+    }
+    const int r = lane & 15;
+    copy_async<4, kCut>(stage + 2 * kTile * S::kRow + lane * 4, sp, !kCut || (r >= v0 && r < v1));
 }
 
 __device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
@@ -122,7 +157,7 @@ template <int FMT, int D>
 __device__ __forceinline__ int key_dim(int c, int s) {
     constexpr int kKB = (FMT == W4KV_INT4 ? D / 2 : D) / 4;
     if (FMT == W4KV_INT4) return 2 * (c * kKB + 4 * (s >> 1)) + 4 * (s & 1);
-    if (kKB == 32) return 16 * (c + 4 * (s >> 2)) + 4 * (s & 3);  // two 16-byte pieces, 64 apart
+    if (kKB == 32) return 16 * (c + 4 * (s >> 2)) + 4 * (s & 3);  // two 16-byte pieces, 64 bytes apart
     return c * kKB + 4 * s;
 }
 
@@ -130,14 +165,14 @@ __device__ __forceinline__ int key_dim(int c, int s) {
 struct Walk {
     Seq s;
     int b, h;         // sequence, key/value head
-    int u, nu;        // next unit of the item, units of the item
-    int64_t rem;      // units of the block not yet walked
-    int take;         // units of the current segment (the item's part in the block's range)
+    int x, nu;        // walked of the item, in cost; its units
+    int64_t rem;      // cost of the block's range not yet walked
+    int u0, u1;       // units of the current segment (the item's part in the block's range)
     int tile, end;    // its tiles: this warp's next one, the first behind it
 };
 
 template <int FMT, int D, int XT, int NT>
-__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
+__global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_kernel(const Attn a) {
     using S = Shape<FMT, D, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -156,22 +191,24 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
     };
     const Range range = block_range<kThreads>(a.b.n, rsm, [&](int b) -> int64_t {
         const Seq s = load_seq(a, b);
-        return s.n > 0 ? int64_t(item_units(s)) * a.c.heads : 0;
+        return s.n > 0 ? int64_t(kItemCost + item_units(s)) * a.c.heads : 0;
     });
     if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     if (range.start == range.end) return;
 
-    // Opens the segment (the part of one item in this block's range) at w.b, w.h, w.u.
+    // Opens the segment (the part of one item in this block's range) at w.b, w.h, w.x.
     auto open = [&](Walk &w) {
-        const int t0 = w.s.lo / 16 + w.u * (kUnit / 16);
-        w.take = static_cast<int>(min(static_cast<int64_t>(w.nu - w.u), w.rem));
-        w.tile = t0 + warp;
-        w.end = min((w.s.hi + 15) / 16, t0 + w.take * (kUnit / 16));
-        w.rem -= w.take;
-        w.u += w.take;
+        const int x1 = static_cast<int>(min(static_cast<int64_t>(w.nu + kItemCost), w.x + w.rem));
+        w.u0 = max(0, w.x - kItemCost);
+        w.u1 = max(0, x1 - kItemCost);
+        w.rem -= x1 - w.x;
+        w.x = x1;
+        const int t0 = w.s.lo / 16;
+        w.tile = t0 + w.u0 * (kUnit / 16) + warp;
+        w.end = min((w.s.hi + 15) / 16, t0 + w.u1 * (kUnit / 16));
     };
     auto next_item = [&](Walk &w) {  // only while w.rem > 0: a later item exists
-        w.u = 0;
+        w.x = 0;
         if (++w.h == a.c.heads) {
             w.h = 0;
             do {
@@ -185,14 +222,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
     w.b = range.b;
     w.s = load_seq(a, w.b);
     w.nu = item_units(w.s);
-    w.h = static_cast<int>(range.off / w.nu);
-    w.u = static_cast<int>(range.off % w.nu);
+    w.h = static_cast<int>(range.off / (w.nu + kItemCost));
+    w.x = static_cast<int>(range.off % (w.nu + kItemCost));
     w.rem = range.end - range.start;
     open(w);
     Walk p = w;  // the producer's walk, ahead of the consumer's
 
     // ---- producer: fragment bytes of one tile per stage ----
-    int p_id = 0, p_rest = 0, issued = 0;
+    int p_id = 0, p_rest = 0;
     bool p_live = true;  // a tile is left to issue
     auto fetch_page = [&]() {
         while (p.tile >= p.end) {  // to the next segment that has a tile for this warp
@@ -208,56 +245,47 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
     };
     fetch_page();
     uint32_t bad_mask = 0;  // per stage: the tile's page number was out of range
+    const uint8_t *k_lane = a.c.k + g * S::kRow + c * (S::kKB < 16 ? S::kKB : 16);
+    const uint8_t *v_lane = a.c.v + 2 * c * S::kRow + g * S::kVB;
+    const float *s_lane = (lane < 16 ? a.c.ks : a.c.vs) + (lane & 15);
+    const int page_rows = a.c.heads * a.c.page;
+    int put = 0;  // stage that is filled next
     auto issue = [&]() {
         if (p_live) {
-            const int slot = issued % S::kStages;
-            const uint32_t dst = ring_u + slot * S::kStage;
-            const bool ok = p_id >= 0 && p_id < a.c.pages;
-            if (!ok && lane == 0) atomicOr(a.status, kStatusBounds);
-            bad_mask = ok ? bad_mask & ~(1u << slot) : bad_mask | (1u << slot);
-            const int64_t r0 = ok ? (int64_t(p_id) * a.c.heads + p.h) * a.c.page + p_rest * kTile : 0;
-            const int kv0 = p.tile * kTile;
-            const int v0 = ok ? max(0, p.s.lo - kv0) : kTile, v1 = p.s.hi - kv0;  // rows in use
-            const uint8_t *kp = a.c.k + r0 * S::kRow, *vp = a.c.v + r0 * S::kRow;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {  // key rows g, g + 8
-                const int r = g + 8 * i;
-                const bool live = r >= v0 && r < v1;
-                if (S::kKB == 32) {
-                    copy_async<16>(dst + (2 * i) * 512 + lane * 16, kp + r * S::kRow + c * 16, live);
-                    copy_async<16>(dst + (2 * i + 1) * 512 + lane * 16, kp + r * S::kRow + 64 + c * 16, live);
-                } else if (S::kKB == 16) {
-                    copy_async<16>(dst + i * 512 + lane * 16, kp + r * S::kRow + c * 16, live);
-                } else {
-                    copy_async<8>(dst + i * 256 + lane * 8, kp + r * S::kRow + c * 8, live);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // value rows 2c, 2c + 1, 2c + 8, 2c + 9
-                const int r = 2 * c + (i & 1) + 8 * (i >> 1);
-                copy_async<S::kVB>(dst + kTile * S::kRow + (i * 32 + lane) * S::kVB,
-                                   vp + r * S::kRow + g * S::kVB, r >= v0 && r < v1);
-            }
-            {  // scale words: 16 of the keys, 16 of the values
-                const int r = lane & 15;
-                copy_async<4>(dst + 2 * kTile * S::kRow + lane * 4,
-                              (lane < 16 ? a.c.ks : a.c.vs) + r0 + r, r >= v0 && r < v1);
+            const uint32_t dst = ring_u + put * S::kStage;
+            const bool ok = static_cast<uint32_t>(p_id) < static_cast<uint32_t>(a.c.pages);
+            const int64_t r0 = int64_t(ok ? p_id : 0) * page_rows + (p.h * a.c.page + p_rest * kTile);
+            const int v0 = p.s.lo - p.tile * kTile, v1 = p.s.hi - p.tile * kTile;  // rows in use
+            if (ok && v0 <= 0 && v1 >= kTile) {
+                bad_mask &= ~(1u << put);
+                copy_tile<S, false>(dst, k_lane + r0 * S::kRow, v_lane + r0 * S::kRow, s_lane + r0, lane, 0, 0);
+            } else {
+                bad_mask = ok ? bad_mask & ~(1u << put) : bad_mask | (1u << put);
+                if (!ok && lane == 0) atomicOr(a.status, kStatusBounds);
+                copy_tile<S, true>(dst, k_lane + r0 * S::kRow, v_lane + r0 * S::kRow, s_lane + r0, lane,
+                                   ok ? v0 : kTile, v1);
             }
             p.tile += kWarps;
             fetch_page();
         }
-        ++issued;
+        put = put + 1 == S::kStages ? 0 : put + 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
     for (int i = 0; i < S::kStages; ++i) issue();
-    int consumed = 0;
+    int get = 0;  // stage that is read next
 
     while (true) {  // segments
+        if (w.u0 == w.u1) {  // none of the item's units
+            if (w.rem == 0) break;
+            next_item(w);
+            open(w);
+            continue;
+        }
         // ---- the item's query rows as B fragments, and what each column sees ----
         uint32_t bq[NT][S::kSteps][2];
-        float f1[NT][2], f2[NT][2], qsum[NT][2];
-        int clo[NT][2], chi[NT][2];
+        float f[NT][2], qsum[NT][2];  // scale * log2(e) without the row's power of two; sum of q
+        int qpos[NT][2];  // position of the column's row
         const int R = w.s.n * a.group;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -278,11 +306,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the row times 2^sh has its largest element in [2^10, 2^11)
+            // the row times 2^sh has its largest element in [2^4, 2^5)
             int sh = 0;
             {
                 const uint32_t t32 = __float_as_uint(widen1<XT>(static_cast<uint16_t>(top)));
-                if (t32 != 0 && t32 < 0x7F800000u) sh = min(120, 137 - static_cast<int>(t32 >> 23));
+                if (t32 != 0 && t32 < 0x7F800000u) sh = min(120, 131 - static_cast<int>(t32 >> 23));
             }
             const float up = pow2i(sh);
             float sum = 0.f;
@@ -311,16 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
             for (int e = 0; e < 2; ++e) {
                 const int s2 = __shfl_sync(0xffffffffu, sh, 8 * c + 4 * e);
                 qsum[nt][e] = FMT == W4KV_INT4 ? __shfl_sync(0xffffffffu, sum, 8 * c + 4 * e) : 0.f;
-                f1[nt][e] = pow2i(-(s2 / 2));
-                f2[nt][e] = pow2i(-(s2 - s2 / 2)) * a.scale_log2;
+                f[nt][e] = pow2i(-s2) * a.scale_log2;
                 const int rr = nt * 8 + 2 * c + e;
                 const int pos = w.s.first + rr / a.group;
-                clo[nt][e] = w.s.lo;
-                chi[nt][e] = w.s.hi;
-                if (a.causal && rr < R) {
-                    chi[nt][e] = min(w.s.hi, pos + 1);
-                    if (a.window > 0) clo[nt][e] = max(w.s.lo, pos + 1 - a.window);
-                }
+                qpos[nt][e] = pos;
             }
         }
         // tiles inside [all_lo, all_hi) are seen whole by every row
@@ -332,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m[nt][e] = -INFINITY;
+                m[nt][e] = kNone;
                 l[nt][e] = 0.f;
             }
 #pragma unroll
@@ -340,18 +362,17 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[nt][t][i] = 0.f;
         }
-        int vexp = 0;  // exponent field of the largest value scale so far: a weight is p * scale * 2^(133 - vexp)
+        int vexp = 7;  // exponent field of the largest value scale so far (at least 7): weights are p * scale * 2^(133 - vexp)
 
         auto consume = [&](auto np_tag) {
             constexpr int NP = decltype(np_tag)::value;
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - NP) : "memory");
             __syncwarp();
-            uint32_t kw[NP][2][S::kKB / 4], vw[NP][4][S::kVB / 4], ksw[NP][2], vsw[NP][2];
-            uint32_t vz[NP][2];  // zero points of the value rows 2c, 2c + 1 and 2c + 8, 2c + 9
+            uint32_t kw[NP][2][S::kKB / 4], ksw[NP][2], vsw[NP][2];
             bool bad[NP];
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
-                const int slot = (consumed + n) % S::kStages;
+                const int slot = get + n < S::kStages ? get + n : get + n - S::kStages;
                 const uint8_t *st = ring + slot * S::kStage;
                 bad[n] = (bad_mask >> slot) & 1;
 #pragma unroll
@@ -369,33 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
                         kw[n][i][0] = v.x, kw[n][i][1] = v.y;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t *vp = st + kTile * S::kRow + (i * 32 + lane) * S::kVB;
-                    if (S::kVB == 16) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(vp);
-                        vw[n][i][0] = v.x, vw[n][i][1] = v.y, vw[n][i][2] = v.z, vw[n][i][3] = v.w;
-                    } else if (S::kVB == 8) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(vp);
-                        vw[n][i][0] = v.x, vw[n][i][1] = v.y;
-                    } else {
-                        vw[n][i][0] = *reinterpret_cast<const uint32_t *>(vp);
-                    }
-                }
                 const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + 2 * kTile * S::kRow);
                 ksw[n][0] = sw[g], ksw[n][1] = sw[g + 8];
                 vsw[n][0] = sw[16 + g], vsw[n][1] = sw[24 + g];
-                if (FMT == W4KV_INT4) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint2 z = *reinterpret_cast<const uint2 *>(sw + 16 + 2 * c + 8 * q);
-                        vz[n][q] = (z.x & 15u) | (z.y & 15u) << 16;
-                    }
-                }
             }
-            __syncwarp();
-#pragma unroll
-            for (int n = 0; n < NP; ++n) issue();
             // ---- S^T = K Q^T ----
             float sc[NP][NT][4];
 #pragma unroll
@@ -422,29 +420,50 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
                     for (int nt = 0; nt < NT; ++nt) mma(sc[n][nt], fa, bq[nt][s][0], bq[nt][s][1]);
                 }
             // ---- scores in base 2, masked ----
-            bool grow = false;
+            bool grow = false, any_cut = false;
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
                 const int kv0 = (w.tile + n * kWarps) * kTile;
                 const bool cut = bad[n] || kv0 < all_lo || kv0 + kTile > all_hi;  // warp-uniform
+                any_cut = any_cut || cut;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int e = i & 1, kw_ = ksw[n][i >> 1];
+                        const int e = i & 1;
+                        const uint32_t kw_ = ksw[n][i >> 1];
                         float x = sc[n][nt][i];
-                        if (FMT == W4KV_INT4) x = fmaf(x, 16777216.f, -static_cast<float>(kw_ & 15) * qsum[nt][e]);
-                        const float ks = FMT == W4KV_INT4 ? int4_scale(kw_) : __uint_as_float(kw_);
-                        x = x * f1[nt][e] * ks * f2[nt][e];
-                        if (cut) {
-                            const int j = kv0 + g + 8 * (i >> 1);
-                            if (bad[n] || j < clo[nt][e] || j >= chi[nt][e]) x = -INFINITY;
-                        }
-                        sc[n][nt][i] = x;
-                        grow = grow || x > m[nt][e] + 8.f;
+                        if (FMT == W4KV_INT4)
+                            x = fmaf(x, 16777216.f, -static_cast<float>(kw_ & 15u) * qsum[nt][e]);
+                        x *= FMT == W4KV_INT4 ? int4_scale(kw_) : __uint_as_float(kw_);
+                        sc[n][nt][i] = x * f[nt][e];
                     }
+                if (cut) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = kv0 + g + 8 * (i >> 1), pos = qpos[nt][i & 1];
+                            if (bad[n] || j < w.s.lo || j >= w.s.hi || (a.causal && j > pos) ||
+                                (a.window > 0 && j <= pos - a.window))
+                                sc[n][nt][i] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) grow = grow || sc[n][nt][i] > m[nt][i & 1] + 8.f;
             }
             // ---- new reference maxima and value exponent, if they moved ----
+            if (any_cut) {  // scales of rows out of use may be anything
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int j = (w.tile + n * kWarps) * kTile + g + 8 * i;
+                        if (bad[n] || j < w.s.lo || j >= w.s.hi) vsw[n][i] = 0;
+                    }
+            }
             uint32_t ve = 0;
 #pragma unroll
             for (int n = 0; n < NP; ++n)
@@ -457,13 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
             const bool vgrow = static_cast<int>(ve) > vexp;
             if (__any_sync(0xffffffffu, grow) || vgrow) {
                 float fv = 1.f;
-                if (vgrow) {  // below 7 the multiplier stays at 2^126
-                    fv = pow2i(max(-126, max(vexp, 7) - max(static_cast<int>(ve), 7)));
+                if (vgrow) {
+                    fv = pow2i(max(-126, vexp - static_cast<int>(ve)));
                     vexp = static_cast<int>(ve);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float f[2];
+                    float fo[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float x = m[nt][e];
@@ -471,18 +490,18 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
                         for (int n = 0; n < NP; ++n) x = fmaxf(x, fmaxf(sc[n][nt][e], sc[n][nt][e + 2]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        f[e] = m[nt][e] == -INFINITY ? 1.f : ex2(m[nt][e] - x);
+                        fo[e] = ex2(m[nt][e] - x);
                         m[nt][e] = x;
-                        l[nt][e] *= f[e];
-                        f[e] *= fv;
+                        l[nt][e] *= fo[e];
+                        fo[e] *= fv;
                     }
 #pragma unroll
                     for (int t = 0; t < S::kSteps; ++t)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[nt][t][i] *= f[i & 1];
+                        for (int i = 0; i < 4; ++i) o[nt][t][i] *= fo[i & 1];
                 }
             }
-            const float vmul = pow2i(133 - max(vexp, 7));
+            const float vmul = pow2i(133 - vexp);
             // ---- weights, transposed into B fragments ----
             uint32_t pb[NP][NT][2];
 #pragma unroll
@@ -497,16 +516,48 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const float x = sc[n][nt][2 * i + e];
-                            const float pe = ex2(x - (m[nt][e] == -INFINITY ? 0.f : m[nt][e]));
+                            const float pe = ex2(x - m[nt][e]);
                             l[nt][e] += pe;
+                            pw[e] = pe * vs;
                             // unseen: exactly zero, whatever the value row's scale is
-                            pw[e] = x == -INFINITY ? 0.f : pe * vs;
+                            if (any_cut && x == -INFINITY) pw[e] = 0.f;
                         }
                         const __half2 h = __floats2half2_rn(pw[0], pw[1]);
                         pb[n][nt][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
                     }
                 }
             // ---- O^T += V^T P^T ----
+            uint32_t vw[NP][4][S::kVB / 4];
+            uint32_t vz[NP][2];  // zero points of the value rows 2c, 2c + 1 and 2c + 8, 2c + 9
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const int slot = get + n < S::kStages ? get + n : get + n - S::kStages;
+                const uint8_t *st = ring + slot * S::kStage;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t *vp = st + kTile * S::kRow + (i * 32 + lane) * S::kVB;
+                    if (S::kVB == 16) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(vp);
+                        vw[n][i][0] = v.x, vw[n][i][1] = v.y, vw[n][i][2] = v.z, vw[n][i][3] = v.w;
+                    } else if (S::kVB == 8) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(vp);
+                        vw[n][i][0] = v.x, vw[n][i][1] = v.y;
+                    } else {
+                        vw[n][i][0] = *reinterpret_cast<const uint32_t *>(vp);
+                    }
+                }
+                if (FMT == W4KV_INT4) {
+                    const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + 2 * kTile * S::kRow);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint2 z = *reinterpret_cast<const uint2 *>(sw + 16 + 2 * c + 8 * q);
+                        vz[n][q] = (z.x & 15u) | (z.y & 15u) << 16;
+                    }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < NP; ++n) issue();
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
                 if (FMT == W4KV_INT4) {
@@ -556,11 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
                     }
                 }
             }
-            consumed += NP;
+            get = get + NP < S::kStages ? get + NP : get + NP - S::kStages;
             w.tile += NP * kWarps;
         };
-        while (w.tile + kWarps < w.end) consume(std::integral_constant<int, 2>());
-        if (w.tile < w.end) consume(std::integral_constant<int, 1>());
+        if (S::kAtOnce == 2)
+            while (w.tile + kWarps < w.end) consume(std::integral_constant<int, 2>());
+        while (w.tile < w.end) consume(std::integral_constant<int, 1>());
 
         // ---- the warps' results together ----
 #pragma unroll
@@ -578,40 +630,38 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Attn a) {
                 }
             }
         __syncthreads();
-        const float vback = pow2i(max(vexp, 7) - 133);  // 1 / vmul
+        const float vback = pow2i(vexp - 133);  // 1 / vmul
         float wgt[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = nt * 8 + 2 * c + e;
-                float M = -INFINITY, L = 0.f;
+                float M = kNone, L = 0.f;
 #pragma unroll
                 for (int q = 0; q < kWarps; ++q) M = fmaxf(M, stat_m[q * S::kTileRows + r]);
-                const float mu = M == -INFINITY ? 0.f : M;
 #pragma unroll
                 for (int q = 0; q < kWarps; ++q)
-                    L += stat_l[q * S::kTileRows + r] * ex2(stat_m[q * S::kTileRows + r] - mu);
-                wgt[nt][e] = L == 0.f ? 0.f : ex2(m[nt][e] - mu) / L;
+                    L += stat_l[q * S::kTileRows + r] * ex2(stat_m[q * S::kTileRows + r] - M);
+                wgt[nt][e] = L == 0.f ? 0.f : ex2(m[nt][e] - M) / L;
             }
         // where the item's units lie among the blocks
-        const bool from_start = w.u == w.take;
-        const bool to_end = w.u == w.nu;
+        const bool from_start = w.u0 == 0;
+        const bool to_end = w.u1 == w.nu;
         const bool whole = from_start && to_end;
         float *slot = a.slots + (2 * int64_t(blockIdx.x) + (from_start ? 1 : 0)) *
                                     slot_floats(S::kTileRows, D);
         if (!whole && from_start && threadIdx.x == 0) {
-            const int64_t last = range.end - w.rem + (w.nu - w.u) - 1;
+            const int64_t last = range.end - w.rem + (w.nu - w.u1) - 1;  // its last unit
             a.desc[blockIdx.x] =
                 make_int4(w.b, w.h, block_of_unit(last, range) - static_cast<int>(blockIdx.x) + 1, 0);
         }
         if (threadIdx.x < S::kTileRows) {
             const int r = threadIdx.x;
-            float M = -INFINITY, L = 0.f;
+            float M = kNone, L = 0.f;
             for (int q = 0; q < kWarps; ++q) M = fmaxf(M, stat_m[q * S::kTileRows + r]);
-            const float mu = M == -INFINITY ? 0.f : M;
             for (int q = 0; q < kWarps; ++q)
-                L += stat_l[q * S::kTileRows + r] * ex2(stat_m[q * S::kTileRows + r] - mu);
+                L += stat_l[q * S::kTileRows + r] * ex2(stat_m[q * S::kTileRows + r] - M);
             if (!whole) {
                 slot[r] = M;
                 slot[S::kTileRows + r] = L;
