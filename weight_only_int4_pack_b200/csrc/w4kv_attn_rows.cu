@@ -21,11 +21,11 @@
 //     dims) as the 16 rows and query rows as the 8 columns: a decode step of
 //     8 heads per key/value head fills the tile; tcgen05's 128 rows would be
 //     15/16 padding.
-//   * every lane copies (cp.async) exactly the code bytes of its own fragments
-//     into its own slots of the warp's ring: contiguous pieces of a row, no
-//     exchange between lanes, no bank conflicts.  Which dim a fragment index
-//     stands for is free (the contraction index of S, the row index of O^T),
-//     so a lane's piece of a row becomes consecutive fragments.
+//   * a tile of 16 tokens is copied (cp.async) as it lies, whole lines, into
+//     swizzled shared memory, and every lane reads its own fragments' bytes:
+//     contiguous pieces of a row.  Which dim a fragment index stands for is
+//     free (the contraction index of S, the row index of O^T), so a lane's
+//     piece of a row becomes consecutive fragments.
 //   * value fragments pair two tokens of one dim: bytes of two rows'
 //     words, merged with byte permutations.
 //   * P^T needs one 8x8 transpose per 8 tokens (movmatrix).
@@ -54,7 +54,7 @@ struct Shape {
     static constexpr int kStage = 2 * kTile * kRow + 128;      // codes, then 32 scale words
     static constexpr int kBlocks = NT == 1 ? 4 : 3;  // blocks per SM
     static constexpr int kAtOnce = 1;                // tiles that a warp takes at a time
-    static constexpr int kStages = kRow == 128 ? 3 : 6;
+    static constexpr int kStages = kRow == 128 ? 3 : 5;
     static constexpr int kSteps = D / 16;  // k steps of S, row tiles of O^T
     static constexpr int kTileRows = 8 * NT;
     static constexpr int kPhase = 32;  // dims joined at a time
@@ -63,55 +63,54 @@ struct Shape {
     static constexpr int kJoin = kWarps * kTileRows * kPad * 4;
     static constexpr int kStats = kWarps * kTileRows * 2 * 4;
     static constexpr int kSmem = kRing + kJoin + kStats + static_cast<int>(sizeof(RangeSmem)) + 16;
+    // the grid is one wave: kBlocks of them (and 1 KB each) fit an SM's 228 KB
+    static_assert(kBlocks * (kSmem + 1024) <= 228 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Copies N bytes; with kCut, or writes N zeros.
-template <int N, bool kCut>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool live) {
-    const int n = live ? N : 0;
-    if (N == 16) {
-        if (kCut)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-        else
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    } else if (kCut) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(N) : "memory");
-    } else {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
-    }
+// Copies 16 bytes; with kCut, or writes 16 zeros.
+template <bool kCut>
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+    if (kCut)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// A tile's fragment bytes and scale words into a stage: the lane's pieces of
-// key rows g, g + 8, of value rows 2c, 2c + 1, 2c + 8, 2c + 9, and scale word
-// `lane` (16 of the keys, 16 of the values).  kp, vp, sp point to the lane's
-// first piece; dst counts the lane in already for 16-byte pieces.  With kCut
-// only rows [v0, v1) are read, the others are zeros.
+// Where the 16-byte piece p of row r of a tile lies in a stage: the pieces that
+// the lanes of a fragment load read together fall into different banks.
+template <int ROW>
+__device__ __forceinline__ int piece_at(int r, int p) {
+    if (ROW == 128) return r * 128 + ((p ^ (r & 7)) << 4);
+    if (ROW == 64) return r * 64 + ((p ^ ((r >> 1) & 3)) << 4);
+    return r * 32 + ((p ^ ((r >> 2) & 1)) << 4);
+}
+
+// A tile's codes (16 rows one after the other: whole lines per instruction)
+// and scale words into a stage.  kp, vp, sp point to the lane's first piece.
+// With kCut only rows [v0, v1) are read, the others are zeros.
 template <class S, bool kCut>
 __device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t *kp, const uint8_t *vp,
                                           const float *sp, int lane, int v0, int v1) {
-    const int g = lane >> 2, c = lane & 3;
-    constexpr int kP = S::kKB < 16 ? S::kKB : 16;  // bytes of a key piece
-    const uint32_t kd = stage + lane * kP, vd = stage + kTile * S::kRow + lane * S::kVB;
+    constexpr int kPieces = S::kRow / 16;
+    const int r0 = lane / kPieces;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool live = !kCut || (g + 8 * i >= v0 && g + 8 * i < v1);
-#pragma unroll
-        for (int j = 0; j < S::kKB / kP; ++j)
-            copy_async<kP, kCut>(kd + (i * (S::kKB / kP) + j) * 32 * kP,
-                                 kp + 8 * i * S::kRow + j * 64, live);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (i & 1) + 8 * (i >> 1);
-        copy_async<S::kVB, kCut>(vd + i * 32 * S::kVB, vp + r * S::kRow,
-                                 !kCut || (2 * c + r >= v0 && 2 * c + r < v1));
+    for (int i = 0; i < S::kRow / 32; ++i) {  // 512 bytes each
+        const int r = r0 + i * (32 / kPieces);
+        const uint32_t at = piece_at<S::kRow>(r, lane % kPieces);
+        const bool live = !kCut || (r >= v0 && r < v1);
+        copy16<kCut>(stage + at, kp + i * 512, live);
+        copy16<kCut>(stage + kTile * S::kRow + at, vp + i * 512, live);
     }
     const int r = lane & 15;
-    copy_async<4, kCut>(stage + 2 * kTile * S::kRow + lane * 4, sp, !kCut || (r >= v0 && r < v1));
+    const uint32_t at = stage + 2 * kTile * S::kRow + lane * 4;
+    if (kCut)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(sp), "r"(r >= v0 && r < v1 ? 4 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(sp) : "memory");
 }
 
 __device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
@@ -157,7 +156,6 @@ template <int FMT, int D>
 __device__ __forceinline__ int key_dim(int c, int s) {
     constexpr int kKB = (FMT == W4KV_INT4 ? D / 2 : D) / 4;
     if (FMT == W4KV_INT4) return 2 * (c * kKB + 4 * (s >> 1)) + 4 * (s & 1);
-    if (kKB == 32) return 16 * (c + 4 * (s >> 2)) + 4 * (s & 3);  // two 16-byte pieces, 64 bytes apart
     return c * kKB + 4 * s;
 }
 
@@ -245,8 +243,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
     };
     fetch_page();
     uint32_t bad_mask = 0;  // per stage: the tile's page number was out of range
-    const uint8_t *k_lane = a.c.k + g * S::kRow + c * (S::kKB < 16 ? S::kKB : 16);
-    const uint8_t *v_lane = a.c.v + 2 * c * S::kRow + g * S::kVB;
+    const uint8_t *k_lane = a.c.k + lane * 16, *v_lane = a.c.v + lane * 16;
     const float *s_lane = (lane < 16 ? a.c.ks : a.c.vs) + (lane & 15);
     const int page_rows = a.c.heads * a.c.page;
     int put = 0;  // stage that is filled next
@@ -376,17 +373,18 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 const uint8_t *st = ring + slot * S::kStage;
                 bad[n] = (bad_mask >> slot) & 1;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 2; ++i) {  // rows g, g + 8: the same piece offsets, 8 rows on
                     if (S::kKB >= 16) {
 #pragma unroll
                         for (int j = 0; j < S::kKB / 16; ++j) {
                             const uint4 v = *reinterpret_cast<const uint4 *>(
-                                st + (i * (S::kKB / 16) + j) * 512 + lane * 16);
+                                st + piece_at<S::kRow>(g, c * (S::kKB / 16) + j) + i * 8 * S::kRow);
                             kw[n][i][4 * j] = v.x, kw[n][i][4 * j + 1] = v.y;
                             kw[n][i][4 * j + 2] = v.z, kw[n][i][4 * j + 3] = v.w;
                         }
                     } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(st + i * 256 + lane * 8);
+                        const uint2 v = *reinterpret_cast<const uint2 *>(
+                            st + piece_at<S::kRow>(g, c >> 1) + (c & 1) * 8 + i * 8 * S::kRow);
                         kw[n][i][0] = v.x, kw[n][i][1] = v.y;
                     }
                 }
@@ -535,7 +533,9 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 const uint8_t *st = ring + slot * S::kStage;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint8_t *vp = st + kTile * S::kRow + (i * 32 + lane) * S::kVB;
+                    const uint8_t *vp = st + kTile * S::kRow + (i >> 1) * 8 * S::kRow +
+                                        piece_at<S::kRow>(2 * c + (i & 1), g * S::kVB / 16) +
+                                        (g * S::kVB) % 16;
                     if (S::kVB == 16) {
                         const uint4 v = *reinterpret_cast<const uint4 *>(vp);
                         vw[n][i][0] = v.x, vw[n][i][1] = v.y, vw[n][i][2] = v.z, vw[n][i][3] = v.w;
