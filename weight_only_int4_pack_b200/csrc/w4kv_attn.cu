@@ -1,10 +1,12 @@
-// w4kv_attn.cu -- w4kv_attention: attention of new rows over the quantized
-// paged cache (semantics: include/w4kv.h).
+// w4kv_attn.cu -- w4kv_attention: argument checks, the choice of kernels, and
+// the join of partial results (semantics: include/w4kv.h).
 //
-// One warp per (row, query head): the lanes hold D / 32 elements of the query
-// each and walk over the cached tokens with a running maximum and sum.
+// Sequences with at most 16 (row, query head) pairs per key/value head go to
+// the row kernel (w4kv_attn_rows.cu), all others to the tiled one
+// (w4kv_attn_tiled.cu).  The numbers of rows live on the device, so the host
+// launches what max_rows and the batch allow, and each kernel leaves out the
+// other's sequences.
 
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include "w4kv_attn.cuh"
@@ -12,94 +14,6 @@
 namespace w4 {
 namespace kv {
 namespace {
-
-template <int FMT, int N>
-__device__ __forceinline__ void load_codes(const uint8_t *row, int lane, uint32_t word, float v[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int k = lane * N + i;
-        if (FMT == W4KV_INT4) {
-            const uint32_t w = reinterpret_cast<const uint32_t *>(row)[k >> 3];
-            const int j = k & 7;
-            v[i] = static_cast<float>(static_cast<int>((w >> (4 * ((j >> 1) + 4 * (j & 1)))) & 15u) -
-                                      static_cast<int>(word & 15u));
-        } else if (FMT == W4KV_INT8) {
-            v[i] = static_cast<float>(reinterpret_cast<const int8_t *>(row)[k]);
-        } else {
-            const __half_raw h = __nv_cvt_fp8_to_halfraw(row[k], __NV_E4M3);
-            v[i] = __half2float(*reinterpret_cast<const __half *>(&h));
-        }
-    }
-}
-
-template <int FMT, int D, int XT>
-__global__ void __launch_bounds__(128)
-attention_kernel(const Attn a, int64_t items, float scale) {
-    const Cache &c = a.c;
-    const Batch &bt = a.b;
-    const uint16_t *Q = a.q;
-    uint16_t *O = a.o;
-    float *lse = a.lse;
-    const int64_t qrs = a.q_row, qhs = a.q_head, ors = a.o_row, ohs = a.o_head, max_rows = a.max_rows;
-    const int heads = a.heads, causal = a.causal, window = a.window;
-    unsigned *status = a.status;
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (item >= items) return;
-    const int t = static_cast<int>(item / heads), h = static_cast<int>(item % heads);
-    const int b = find_sequence(bt.cu, bt.n, t, lane);
-    if (b < 0) return;
-    if (t - __ldg(bt.cu + b) >= max_rows) {
-        if (lane == 0) atomicOr(status, kStatusBounds);
-        return;
-    }
-    const Seq sq = load_seq(a, b);
-    if (sq.n == 0) return;
-    const int len = __ldg(bt.lens + b);
-    const int pos = len - (__ldg(bt.cu + b + 1) - t);
-    const int hi = causal ? pos + 1 : len;
-    const int lo = window > 0 ? max(0, pos + 1 - window) : 0;
-    const int kvh = h / (heads / c.heads);
-    float q[N], o[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        q[i] = widen1<XT>(Q[t * qrs + h * qhs + lane * N + i]);
-        o[i] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int j = lo; j < hi; ++j) {
-        const int64_t r0 = row_of(c, bt, b, j);
-        if (r0 < 0) {
-            if (lane == 0) atomicOr(status, kStatusBounds);
-            if (j / c.page >= bt.width) break;
-            continue;
-        }
-        const int64_t r = r0 + int64_t(kvh) * c.page;
-        const uint32_t kw = __float_as_uint(c.ks[r]), vw = __float_as_uint(c.vs[r]);
-        float kk[N], vv[N];
-        load_codes<FMT, N>(c.k + r * c.row_bytes, lane, kw, kk);
-        load_codes<FMT, N>(c.v + r * c.row_bytes, lane, vw, vv);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s = fmaf(q[i], kk[i], s);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= (FMT == W4KV_INT4 ? int4_scale(kw) : __uint_as_float(kw)) * scale;
-        const float vs = FMT == W4KV_INT4 ? int4_scale(vw) : __uint_as_float(vw);
-        const float mn = fmaxf(m, s);
-        const float f = m == -INFINITY ? 0.f : expf(m - mn);
-        const float p = expf(s - mn);
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = o[i] * f + p * vs * vv[i];
-        m = mn;
-    }
-    const float inv = l > 0.f || isnan(l) ? 1.f / l : 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) O[t * ors + h * ohs + lane * N + i] = narrow1<XT>(o[i] * inv);
-    if (lse && lane == 0) lse[int64_t(t) * heads + h] = l > 0.f || isnan(l) ? m + logf(l) : -INFINITY;
-}
 
 // Item that starts in block blockIdx.x and ends in a later one: the weighted
 // mean of its blocks' normalized outputs.
@@ -160,25 +74,33 @@ int launch_combine(const Attn &a, int grid, int tile, int dim, int xt, cudaStrea
 
 namespace {
 
-// Tile of the row kernel for sequences of up to `pairs` (row, head) pairs per
-// key/value head: 8 or 16, or 0 when none of the batch can be that small.
-struct Plan {
-    int rows_tile = 0;  // 8 or 16: the row kernel runs
-    bool tiled = false; // the tiled kernel runs
+// Which kernels run, and the workspace: per launch its descriptors, then its slots.
+struct Launch {
+    int tile = 0;  // rows of a slot; 0: the launch is left out
     int grid = 0;
-    size_t slots = 0, total = 0;  // bytes: partials per launch, workspace
+    size_t begin = 0, slots = 0;  // byte offsets of descriptors and slots
 };
+struct Plan {
+    Launch rows, tiled;
+    size_t total = 0;
+};
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 Plan make_plan(const DeviceInfo &d, int dim, int64_t batch, int64_t max_rows, int group) {
     Plan p;
     const int64_t pairs = max_rows * group;
-    p.tiled = pairs > 16;
-    if (pairs <= 8) p.rows_tile = 8;
-    else if (pairs <= 16 || (batch > 1 && group <= 16)) p.rows_tile = 16;
-    p.grid = (p.rows_tile == 8 ? 4 : 3) * d.sm_count;
-    const size_t desc = (size_t(p.grid) * 16 + 255) & ~size_t(255);
-    p.slots = 2 * size_t(p.grid) * slot_floats(p.rows_tile, dim) * 4;
-    p.total = p.rows_tile ? desc + ((p.slots + 255) & ~size_t(255)) : 0;
+    if (pairs <= 8) p.rows.tile = 8;
+    else if (pairs <= 16 || (batch > 1 && group <= 16)) p.rows.tile = 16;
+    if (pairs > 16) p.tiled.tile = kTiledRows;
+    p.rows.grid = rows_blocks_per_sm(p.rows.tile) * d.sm_count;
+    p.tiled.grid = d.sm_count;
+    for (Launch *l : {&p.rows, &p.tiled}) {
+        if (!l->tile) continue;
+        l->begin = p.total;
+        l->slots = l->begin + up256(size_t(l->grid) * sizeof(int4));
+        p.total = l->slots + up256(2 * size_t(l->grid) * slot_floats(l->tile, dim) * 4);
+    }
     return p;
 }
 
@@ -249,27 +171,26 @@ int w4kv_attention(const w4kv_cache *cache, const w4kv_batch *batch, const void 
     a.window = window > 0x7FFFFFFF ? 0 : static_cast<int>(window);
     a.page_magic = page_magic(a.c.page);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (p.rows_tile) {
-        a.min_rows = 0, a.max_served = p.rows_tile;
-        a.desc = static_cast<int4 *>(workspace);
-        a.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
-                                            ((size_t(p.grid) * 16 + 255) & ~size_t(255)));
-        if ((st = launch_rows_attention(a, cache->fmt, D, xt, p.rows_tile, p.grid, s)) != W4_OK) return st;
-        if ((st = launch_combine(a, p.grid, p.rows_tile, D, xt, s)) != W4_OK) return st;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    auto partials = [&](const Launch &l) {
+        a.desc = reinterpret_cast<int4 *>(ws + l.begin);
+        a.slots = reinterpret_cast<float *>(ws + l.slots);
+    };
+    a.min_rows = 0;
+    if (p.rows.tile) {
+        partials(p.rows);
+        a.max_served = p.rows.tile;
+        if ((st = launch_rows_attention(a, cache->fmt, D, xt, p.rows.tile, p.rows.grid, s)) != W4_OK) return st;
+        if ((st = launch_combine(a, p.rows.grid, p.rows.tile, D, xt, s)) != W4_OK) return st;
+        a.min_rows = p.rows.tile;
     }
-    if (!p.tiled) return W4_OK;
-    a.min_rows = p.rows_tile;
-    a.max_served = int64_t(1) << 62;
-    const int64_t items = rows * heads;
-    if (items > int64_t(0x7FFFFFFF)) return set_error(W4_ERR_INVALID_ARG, fn, "rows * heads too large");
-    const unsigned grid = static_cast<unsigned>((items + 3) / 4);
-#define RUN(F, DD, X) attention_kernel<F, DD, X><<<grid, 128, 0, s>>>(a, items, scale)
-#define RUN_X(F, DD) if (xt == W4_F16) RUN(F, DD, W4_F16); else RUN(F, DD, W4_BF16)
-#define RUN_D(F) if (D == 64) { RUN_X(F, 64); } else { RUN_X(F, 128); }
-    if (cache->fmt == W4KV_INT8) { RUN_D(W4KV_INT8) }
-    else if (cache->fmt == W4KV_E4M3) { RUN_D(W4KV_E4M3) }
-    else { RUN_D(W4KV_INT4) }
-    return cuda_status(cudaGetLastError());
+    if (p.tiled.tile) {
+        partials(p.tiled);
+        a.max_served = int64_t(1) << 62;
+        if ((st = launch_tiled_attention(a, cache->fmt, D, xt, p.tiled.grid, s)) != W4_OK) return st;
+        if ((st = launch_combine(a, p.tiled.grid, p.tiled.tile, D, xt, s)) != W4_OK) return st;
+    }
+    return W4_OK;
 }
 
 }  // extern "C"

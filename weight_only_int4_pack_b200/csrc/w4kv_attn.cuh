@@ -189,7 +189,12 @@ inline uint32_t page_magic(int page) {
 // attention kernel, with that kernel's grid and `tile` rows per slot.
 int launch_combine(const Attn &a, int grid, int tile, int dim, int xt, cudaStream_t stream);
 
+// Items of up to 256 (row, head) pairs on tcgen05 (w4kv_attn_tiled.cu).
+constexpr int kTiledRows = 256;
+int launch_tiled_attention(const Attn &a, int fmt, int dim, int xt, int grid, cudaStream_t stream);
+
 // Items of up to 16 (row, head) pairs: warp-level MMA (w4kv_attn_rows.cu).
+constexpr int rows_blocks_per_sm(int tile) { return tile == 8 ? 4 : 3; }
 int launch_rows_attention(const Attn &a, int fmt, int dim, int xt, int tile, int grid,
                           cudaStream_t stream);
 

@@ -52,7 +52,7 @@ struct Shape {
     static constexpr int kRow = FMT == W4KV_INT4 ? D / 2 : D;  // code bytes of a row
     static constexpr int kKB = kRow / 4, kVB = kRow / 8;       // a lane's bytes of a key / value row
     static constexpr int kStage = 2 * kTile * kRow + 128;      // codes, then 32 scale words
-    static constexpr int kBlocks = NT == 1 ? 4 : 3;  // blocks per SM
+    static constexpr int kBlocks = rows_blocks_per_sm(8 * NT);
     static constexpr int kAtOnce = 1;                // tiles that a warp takes at a time
     static constexpr int kStages = kRow == 128 ? 3 : 5;
     static constexpr int kSteps = D / 16;  // k steps of S, row tiles of O^T

@@ -1,0 +1,996 @@
+// w4kv_attn_tiled.cu -- attention of chunks of new rows over the quantized
+// cache on the 5th-generation tensor cores.
+//
+// An item is a key/value head of a sequence and up to 256 (row, query head)
+// pairs: two tiles A and B of 128 rows, that share every dequantized key and
+// value tile of 128 cached tokens (a step).  Mathematics as in
+// w4kv_attn_rows.cu (running maximum that moves by 2^8 at least, weights held
+// relative to the largest value scale), with
+//     S = Q K^T       tcgen05.mma, both operands in shared memory, fp32 in TMEM
+//     O += P V        tcgen05.mma, P (fp16) read from TMEM, V in shared memory
+// Codes are widened exactly to fp16 (INT4 as u - z); the scales are applied to
+// S's columns and to P's, in fp32.  Tensor memory: S_A, S_B (128 columns each,
+// overwritten by P_A, P_B), O_A, O_B.
+//
+// An item of at most 128 rows runs both streams on the same rows: A takes the
+// even steps and B the odd ones, and their results are joined at the end, so
+// that the tensor cores and the softmax still alternate.
+//
+// Warps (18): 0-3 softmax of A (a row per thread), 4-7 of B; 8-15 read codes
+// from the pages (one step ahead, in registers) and widen them into the
+// swizzled operand tiles (K and V, two stages each; V is the MN-major operand,
+// so both have the layout of the rows as they lie); 16 issues the MMAs (one
+// thread); 17 prepares the steps' scales.  The MMA order is S_A(0) S_B(0), then
+// per step O_A, S_A(next), O_B, S_B(next): while one stream's softmax runs the
+// tensor cores work on the other's.
+//
+// What bounds it: per step and tile 1024 cycles of tensor cores
+// (2 x 128 x 128 x dim / 4096 a cycle at dim 128), 1024 cycles of exp2 (128 x
+// 128 / 16 a cycle) and about 800 of instruction issue; widening costs about
+// 400 more per step.  Every mbarrier wait is bounded.
+
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "w4_tc.cuh"
+#include "w4kv_attn.cuh"
+
+namespace w4 {
+namespace kv {
+namespace {
+
+using namespace tc;
+
+constexpr int kM = 128;              // rows of a tile (MMA M, TMEM lanes)
+constexpr int kTileRows = kTiledRows;  // rows of an item
+static_assert(kTileRows == 2 * kM, "two tiles");
+constexpr int kStep = kUnit;         // cached tokens per step (MMA N of S, K of P V)
+constexpr int kStages = 2;           // operand stages of K and of V
+constexpr int kScaleStages = 4;
+constexpr int kWidenWarps = 8;
+constexpr int kThreads = 32 * (8 + kWidenWarps + 4);  // warps 18 and 19 only complete a warpgroup
+// Registers per thread: launched with 96 x 640 = 61440, and split into
+// 144 x 256 (softmax) + 72 x 256 (widening) + 48 x 128 = 61440.
+constexpr int kRegSoftmax = 144, kRegWiden = 72, kRegRest = 48;
+static_assert(kRegSoftmax * 256 + kRegWiden * 256 + kRegRest * 128 <= 96 * kThreads, "register split");
+constexpr int kTmemCols = 512;
+
+// ---- items ------------------------------------------------------------------------------------
+
+struct Walk {
+    Seq s;
+    int b, h, tile;      // sequence, key/value head, row tile
+    int tiles, nu;       // row tiles of the sequence; units of the item
+    int r0, R;           // first (row, head) pair of the tile, pairs
+    int lo, hi;          // cached positions its rows see; lo a multiple of 16
+    int x;               // walked of the item, in cost
+    int64_t rem;         // cost of the block's range not yet walked
+    int u0, u1;          // units of the current segment
+};
+
+__device__ __forceinline__ void tile_bounds(const Attn &a, const Seq &s, int tile, int *lo, int *hi) {
+    const int64_t r0 = int64_t(tile) * kTileRows;
+    const int64_t r1 = min(int64_t(s.n) * a.group, r0 + kTileRows) - 1;
+    *hi = a.causal ? min(s.hi, max(0, s.first + static_cast<int>(r1 / a.group) + 1)) : s.hi;
+    *lo = a.window > 0 ? max(0, s.first + static_cast<int>(r0 / a.group) + 1 - a.window) : 0;
+    *lo = min(*lo, *hi) & ~15;
+}
+
+__device__ __forceinline__ int tile_units(const Attn &a, const Seq &s, int tile) {
+    int lo, hi;
+    tile_bounds(a, s, tile, &lo, &hi);
+    return max(1, (hi - lo + kStep - 1) / kStep);
+}
+
+__device__ __forceinline__ int seq_tiles(const Attn &a, const Seq &s) {
+    return static_cast<int>((int64_t(s.n) * a.group + kTileRows - 1) / kTileRows);
+}
+
+__device__ __forceinline__ void set_item(const Attn &a, Walk &w) {
+    tile_bounds(a, w.s, w.tile, &w.lo, &w.hi);
+    w.nu = max(1, (w.hi - w.lo + kStep - 1) / kStep);
+    w.r0 = w.tile * kTileRows;
+    w.R = static_cast<int>(min(static_cast<int64_t>(kTileRows), int64_t(w.s.n) * a.group - w.r0));
+}
+
+// Opens the segment (the part of one item in the block's range) at w.x.
+__device__ __forceinline__ void open_segment(Walk &w) {
+    const int x1 = static_cast<int>(min(static_cast<int64_t>(w.nu + kItemCost), w.x + w.rem));
+    w.u0 = max(0, w.x - kItemCost);
+    w.u1 = max(0, x1 - kItemCost);
+    w.rem -= x1 - w.x;
+    w.x = x1;
+}
+
+// To the next segment with units; false when the range is walked.
+__device__ __forceinline__ bool next_segment(const Attn &a, Walk &w) {
+    do {
+        if (w.rem == 0) return false;
+        w.x = 0;
+        if (++w.tile == w.tiles) {
+            w.tile = 0;
+            if (++w.h == a.c.heads) {
+                w.h = 0;
+                do {
+                    if (w.b + 1 < a.b.n) ++w.b;
+                    w.s = load_seq(a, w.b);
+                } while (w.s.n == 0 && w.b + 1 < a.b.n);
+                w.tiles = max(1, seq_tiles(a, w.s));
+            }
+        }
+        set_item(a, w);
+        open_segment(w);
+    } while (w.u0 == w.u1);
+    return true;
+}
+
+__device__ __forceinline__ bool first_segment(const Attn &a, const Range &r, Walk &w) {
+    w.b = r.b;
+    w.s = load_seq(a, w.b);
+    w.tiles = max(1, seq_tiles(a, w.s));
+    int64_t per_head = 0;
+    for (int t = 0; t < w.tiles; ++t) per_head += kItemCost + tile_units(a, w.s, t);
+    w.h = static_cast<int>(r.off / per_head);
+    int64_t x = r.off - w.h * per_head;
+    for (w.tile = 0;; ++w.tile) {
+        set_item(a, w);
+        if (x < w.nu + kItemCost || w.tile + 1 >= w.tiles) break;
+        x -= w.nu + kItemCost;
+    }
+    w.x = static_cast<int>(x);
+    w.rem = r.end - r.start;
+    open_segment(w);
+    return w.u0 < w.u1 || next_segment(a, w);
+}
+
+// Steps of the current segment that stream t takes part in: a prefix.
+__device__ __forceinline__ int stream_steps(const Attn &a, const Walk &w, int t) {
+    const int ns = w.u1 - w.u0;
+    if (t == 1 || w.R <= kM || !a.causal) return ns;
+    const int hi = min(w.hi, w.s.first + (w.r0 + kM - 1) / a.group + 1);  // tile A sees less
+    return min(ns, max(0, (hi - w.lo + kStep - 1) / kStep - w.u0));
+}
+
+// The warp's walk in shared memory, moved by lane 0.
+__device__ __forceinline__ bool warp_next(const Attn &a, Walk *w) {
+    __syncwarp();
+    int more = 0;
+    if ((threadIdx.x & 31) == 0) more = next_segment(a, *w);
+    more = __shfl_sync(0xffffffffu, more, 0);
+    __syncwarp();
+    return more != 0;
+}
+
+struct alignas(16) Control {
+    float ks[kScaleStages][kStep];  // key scales times scale * log2(e)
+    float vs[kScaleStages][kStep];  // value scales times 2^(133 - vexp)
+    float stat[2][2][kM];           // [stream][maximum, sum][row], to join split streams
+    int vexp[kScaleStages];         // exponent field the value scales are relative to
+    uint32_t bad[kScaleStages];     // bit i: tokens 16 i .. 16 i + 15 have no page
+    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t sc_full[kScaleStages], sc_empty[kScaleStages], joined;
+    Walk walk[8 + kWidenWarps + 2];  // of each warp: read by all its lanes, moved by lane 0
+    RangeSmem range;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+template <int D>
+struct Layout {
+    static constexpr int kBlock = 128 * 128;  // 128 rows of 64 fp16: the swizzled unit
+    static constexpr int kBlocks = D / 64;
+    static constexpr int kTile = kBlocks * kBlock;
+    static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile;
+    static constexpr int kControl = kV + kStages * kTile;
+    // at least 120 KB, so that one block (all of tensor memory) is on an SM
+    static constexpr int kUsed = kControl + static_cast<int>(sizeof(Control)) + 1024;
+    static constexpr int kSmem = kUsed < 120 * 1024 ? 120 * 1024 : kUsed;
+};
+
+// ---- instructions ------------------------------------------------------------------------------
+
+// kind::f16, D f32, A and B fp16, M = 128; kTransB: B is MN-major.
+template <int N, bool kTransB>
+__host__ __device__ constexpr uint32_t instr_desc() {
+    return (1u << 4) | (kTransB ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(kM >> 4) << 24);
+}
+
+// MN-major operand, 128-byte swizzle: 64 elements of MN per 128-byte row, 8 rows
+// (k) 1024 bytes apart, the next 64 elements `kBlock` bytes on.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t block) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
+    d |= static_cast<uint64_t>(block >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Pairs of fp32 in one 64-bit register.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Byte offset of 16-byte chunk `chunk` (8 fp16) of row r in a 128-byte-swizzled block.
+__device__ __forceinline__ int swz(int r, int chunk) { return r * 128 + ((chunk ^ (r & 7)) << 4); }
+
+// ---- widening -----------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Four codes -> two fp16 pairs.
+template <int FMT>
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+    uint2 r;
+    if (FMT == W4KV_INT8) {  // 1152 + q as fp16 bits 0x64(q ^ 0x80), then - 1152
+        const uint32_t x = w ^ 0x80808080u;
+        r.x = hsub2u(__byte_perm(x, 0x64646464u, 0x4140), 0x64806480u);
+        r.y = hsub2u(__byte_perm(x, 0x64646464u, 0x4342), 0x64806480u);
+    } else {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(r.x), "=r"(r.y)
+            : "r"(w));
+    }
+    return r;
+}
+
+// Eight INT4 codes -> u - z in dim order; zb = 1024 + z in both halves.
+__device__ __forceinline__ uint4 widen8_int4(uint32_t w, uint32_t zb) {
+    uint4 r;
+    r.x = hsub2u((w & 0x000F000Fu) | 0x64006400u, zb);
+    r.y = hsub2u(((w >> 4) & 0x000F000Fu) | 0x64006400u, zb);
+    r.z = hsub2u(((w >> 8) & 0x000F000Fu) | 0x64006400u, zb);
+    r.w = hsub2u(((w >> 12) & 0x000F000Fu) | 0x64006400u, zb);
+    return r;
+}
+
+template <int FMT, int D, int XT>
+__global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
+    using L = Layout<D>;
+    constexpr int kRow = FMT == W4KV_INT4 ? D / 2 : D;  // code bytes of a row
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    Control *sm = reinterpret_cast<Control *>(base + L::kControl);
+    volatile int *abort_flag = &sm->abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&sm->q_full[t]), kM);
+            mbar_init(smem_u32(&sm->s_full[t]), 1);
+            mbar_init(smem_u32(&sm->p_full[t]), kM);
+            mbar_init(smem_u32(&sm->pv_done[t]), 1);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sm->k_full[i]), 32 * kWidenWarps);
+            mbar_init(smem_u32(&sm->k_empty[i]), 1);
+            mbar_init(smem_u32(&sm->v_full[i]), 32 * kWidenWarps);
+            mbar_init(smem_u32(&sm->v_empty[i]), 1);
+        }
+        for (int i = 0; i < kScaleStages; ++i) {
+            mbar_init(smem_u32(&sm->sc_full[i]), 1);
+            mbar_init(smem_u32(&sm->sc_empty[i]), 8);
+        }
+        mbar_init(smem_u32(&sm->joined), 2 * kM);
+        sm->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    const Range range = block_range<kThreads>(a.b.n, &sm->range, [&](int b) -> int64_t {
+        const Seq s = load_seq(a, b);
+        if (s.n == 0) return 0;
+        const int tiles = seq_tiles(a, s);
+        int64_t cost = 0;
+        for (int t = 0; t < tiles; ++t) cost += kItemCost + tile_units(a, s, t);
+        return cost * a.c.heads;
+    });
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (range.start == range.end) return;  // the whole block
+    if (warp == 16) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sm->tmem)),
+                     "n"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem;
+    const uint32_t tS = tmem, tO = tmem + 2 * kStep;  // + 128 t
+
+    Walk &w = sm->walk[min(warp, 8 + kWidenWarps + 1)];
+    bool more = false;
+    if (warp < 8 + kWidenWarps + 2) {
+        int first = 0;
+        if (lane == 0) first = first_segment(a, range, w);
+        more = __shfl_sync(0xffffffffu, first, 0) != 0;
+        __syncwarp();
+    }
+
+    if (warp < 8) {
+        // =============================== softmax ===============================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax) : "memory");
+        const int t = warp >> 2, row = threadIdx.x & (kM - 1);
+        const uint32_t lane_bits = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane quarter
+        const uint32_t s_col = tS + t * kStep + lane_bits, o_col = tO + t * 128 + lane_bits;
+        uint32_t step_no = 0, own_no = 0, joins = 0;
+        bool ok = true;
+        auto join = [&]() {  // both streams' warps, bounded like every wait
+            mbar_arrive(smem_u32(&sm->joined));
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->joined), joins & 1, abort_flag, a.status));
+            ++joins;
+        };
+        for (; more && ok; more = warp_next(a, &w)) {
+            const bool split = w.R <= kM;
+            const int r = split ? row : t * kM + row;  // of the item
+            const bool live = r < w.R;
+            const int rr = w.r0 + r;
+            const int token = rr / a.group, head = w.h * a.group + rr - token * a.group;
+            // ---- the query row: scaled by a power of two, fp16, swizzled ----
+            float fr;
+            {
+                const uint16_t *qp = a.q + int64_t(w.s.row0 + token) * a.q_row + head * a.q_head;
+                uint32_t top = 0;
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qp) + i);
+                        const uint32_t x = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                                    __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+                        top = max(top, max(x & 0xFFFFu, x >> 16));
+                    }
+                }
+                int sh = 0;  // the row times 2^sh has its largest element in [2^4, 2^5)
+                const uint32_t t32 = __float_as_uint(widen1<XT>(static_cast<uint16_t>(top)));
+                if (t32 != 0 && t32 < 0x7F800000u) sh = min(120, 131 - static_cast<int>(t32 >> 23));
+                const float up = pow2i(sh);
+                fr = pow2i(-sh);
+                uint8_t *qs = base + L::kQ + t * L::kTile;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    float e[8];
+                    widen8<XT>(live ? __ldg(reinterpret_cast<const uint4 *>(qp) + i) : make_uint4(0, 0, 0, 0), e);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __half2 p = __floats2half2_rn(e[2 * j] * up, e[2 * j + 1] * up);
+                        h[j] = *reinterpret_cast<const uint32_t *>(&p);
+                    }
+                    *reinterpret_cast<uint4 *>(qs + (i / 8) * L::kBlock + swz(row, i & 7)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                fence_proxy_async();
+                mbar_arrive(smem_u32(&sm->q_full[t]));
+            }
+            // ---- what the row sees: [clo, chi); what all rows of the warp see: [all_lo, all_hi) ----
+            const int pos = w.s.first + token;
+            int clo = w.lo, chi = w.hi;
+            if (a.window > 0) clo = max(clo, pos + 1 - a.window);
+            if (a.causal) chi = min(chi, pos + 1);
+            if (!live) clo = w.lo, chi = w.hi;
+            clo = max(clo, w.s.lo);
+            const int all_lo = __reduce_max_sync(0xffffffffu, clo);
+            const int all_hi = __reduce_min_sync(0xffffffffu, chi);
+            const bool any_live = __any_sync(0xffffffffu, live);
+
+            float m = kNone, l = 0.f;
+            int vcur = 7, own = 0;
+            const int ns = w.u1 - w.u0, mine = stream_steps(a, w, t), kv_base = w.lo + w.u0 * kStep;
+            for (int j = 0; j < ns && ok; ++j, ++step_no) {
+                const int sc = step_no % kScaleStages;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->sc_full[sc]),
+                                                       (step_no / kScaleStages) & 1, abort_flag, a.status));
+                if (!ok) break;
+                if (split ? (j & 1) == t : j < mine) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->s_full[t]), own_no & 1, abort_flag, a.status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (any_live) {
+                        const int kv0 = kv_base + j * kStep;
+                        const uint32_t bad = sm->bad[sc];
+                        const bool cut = bad != 0 || kv0 < all_lo || kv0 + kStep > all_hi;
+                        auto seen = [&](int c) {  // bits of the 16 tokens from kv0 + 16 c
+                            const int lo = clo - (kv0 + 16 * c), hi = chi - (kv0 + 16 * c);
+                            if (lo >= 16 || hi <= 0 || ((bad >> c) & 1)) return 0u;
+                            return (0xFFFFu << max(lo, 0)) & (0xFFFFu >> (16 - min(hi, 16)));
+                        };
+                        const ulonglong2 *ks2 = reinterpret_cast<const ulonglong2 *>(sm->ks[sc]);
+                        const ulonglong2 *vs2 = reinterpret_cast<const ulonglong2 *>(sm->vs[sc]);
+                        // 16 scores in units of the row's power of two
+                        auto scores = [&](const uint32_t (&s)[16], int c, uint64_t (&x)[8]) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const ulonglong2 k = ks2[4 * c + i];
+                                x[2 * i] = mul2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k.x);
+                                x[2 * i + 1] = mul2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k.y);
+                            }
+                        };
+                        // pass 1: the row's largest score
+                        float top = -INFINITY;
+                        if (!cut) {
+                            uint32_t buf[2][16];  // 16 columns of S while the next 16 are on their way
+                            tmem_ld16(s_col, buf[0]);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                tmem_wait_ld();
+                                if (c < 7) tmem_ld16(s_col + 16 * (c + 1), buf[(c + 1) & 1]);
+                                uint64_t x[8];
+                                scores(buf[c & 1], c, x);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(unpack2(x[i]).x, unpack2(x[i]).y));
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t s[16];
+                                tmem_ld16(s_col + 16 * c, s);
+                                tmem_wait_ld();
+                                uint64_t x[8];
+                                scores(s, c, x);
+                                const uint32_t bits = seen(c);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    if ((bits >> (2 * i)) & 1) top = fmaxf(top, unpack2(x[i]).x);
+                                    if ((bits >> (2 * i)) & 2) top = fmaxf(top, unpack2(x[i]).y);
+                                }
+                                __syncwarp();
+                            }
+                        }
+                        top *= fr;
+                        // a new reference maximum or value exponent: rescale O
+                        const int ve = sm->vexp[sc];
+                        const bool grow = top > m + 8.f;
+                        if (__any_sync(0xffffffffu, grow) || ve != vcur) {
+                            const float mn = fmaxf(m, top);
+                            float f = ex2(m - mn);
+                            m = mn;
+                            l *= f;
+                            if (ve != vcur) f *= pow2i(max(-126, vcur - ve));
+                            vcur = ve;
+                            if (own > 0) {
+                                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->pv_done[t]), (own_no - 1) & 1,
+                                                                       abort_flag, a.status));
+                                if (!ok) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int c = 0; c < D / 32; ++c) {
+                                    uint32_t o[32];
+                                    tmem_ld32(o_col + 32 * c, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tmem_st32(o_col + 32 * c, o);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                        // pass 2: weights
+                        const uint64_t fr2 = pack2(fr, fr), m2 = pack2(-m, -m);
+                        uint64_t l2 = 0;
+                        // eight pairs of scores -> weights; adds the unscaled ones to l2
+                        auto weights = [&](const uint64_t (&x)[8], int c, uint32_t (&p)[8]) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const ulonglong2 v = vs2[4 * c + i];
+                                const float2 x0 = unpack2(fma2(x[2 * i], fr2, m2)), x1 = unpack2(fma2(x[2 * i + 1], fr2, m2));
+                                const uint64_t p0 = pack2(ex2(x0.x), ex2(x0.y)), p1 = pack2(ex2(x1.x), ex2(x1.y));
+                                l2 = add2(l2, p0);
+                                l2 = add2(l2, p1);
+                                const float2 w0 = unpack2(mul2(p0, v.x)), w1 = unpack2(mul2(p1, v.y));
+                                const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
+                                p[2 * i] = *reinterpret_cast<const uint32_t *>(&h0);
+                                p[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+                            }
+                        };
+                        if (!cut) {
+                            uint32_t buf[2][16];
+                            tmem_ld16(s_col, buf[0]);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                tmem_wait_ld();
+                                if (c < 7) tmem_ld16(s_col + 16 * (c + 1), buf[(c + 1) & 1]);
+                                uint64_t x[8];
+                                scores(buf[c & 1], c, x);
+                                uint32_t p[8];
+                                weights(x, c, p);
+                                tmem_st8(s_col + 8 * c, p);
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t s[16];
+                                tmem_ld16(s_col + 16 * c, s);
+                                tmem_wait_ld();
+                                uint64_t x[8];
+                                scores(s, c, x);
+                                const uint32_t bits = seen(c);
+                                __syncwarp();
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float2 y = unpack2(x[i]);
+                                    x[i] = pack2((bits >> (2 * i)) & 1 ? y.x : -INFINITY,
+                                                 (bits >> (2 * i)) & 2 ? y.y : -INFINITY);
+                                }
+                                uint32_t p[8];
+                                weights(x, c, p);
+                                // unseen: exactly zero, whatever the value row's scale is
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const uint32_t two = (bits >> (2 * i)) & 3u;
+                                    p[i] &= (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+                                }
+                                tmem_st8(s_col + 8 * c, p);
+                            }
+                        }
+                        const float2 lp = unpack2(l2);
+                        l += lp.x + lp.y;
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&sm->p_full[t]));
+                    ++own;
+                    ++own_no;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm->sc_empty[sc]));
+            }
+            if (!ok) break;
+            // ---- the result ----
+            if (own > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->pv_done[t]), (own_no - 1) & 1, abort_flag, a.status));
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const bool from_start = w.u0 == 0, to_end = w.u1 == w.nu, whole = from_start && to_end;
+            float *slot = a.slots + (2 * int64_t(blockIdx.x) + (from_start ? 1 : 0)) * slot_floats(kTileRows, D);
+            if (!whole && from_start && threadIdx.x == 0) {
+                const int64_t last = range.end - w.rem + (w.nu - w.u1) - 1;  // its last unit
+                a.desc[blockIdx.x] = make_int4(w.b, w.h, block_of_unit(last, range) - static_cast<int>(blockIdx.x) + 1, w.tile);
+            }
+            float M = m, Lsum = l, weight;
+            float *joined = reinterpret_cast<float *>(base + L::kQ);  // [D][128], over both query tiles
+            if (split) {
+                sm->stat[t][0][row] = m;
+                sm->stat[t][1][row] = l;
+                join();
+                if (!ok) break;
+                const float m2 = sm->stat[1 - t][0][row], l2 = sm->stat[1 - t][1][row];
+                M = fmaxf(m, m2);
+                Lsum = l * ex2(m - M) + l2 * ex2(m2 - M);
+                weight = Lsum == 0.f ? 0.f : ex2(m - M) / Lsum;
+            } else {
+                weight = l == 0.f ? 0.f : 1.f / l;
+            }
+            const float vback = pow2i(vcur - 133);
+            auto output = [&](auto add) {  // the row's normalized output, in chunks of 32 dims
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (own > 0) {
+                        tmem_ld32(o_col + 32 * c, o);
+                        tmem_wait_ld();
+                    }
+                    float x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = add(32 * c + i, own > 0 ? __uint_as_float(o[i]) * weight * vback : 0.f);
+                    if (live && whole) {
+                        uint16_t *op = a.o + int64_t(w.s.row0 + token) * a.o_row + head * a.o_head + 32 * c;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                h[q] = narrow1<XT>(x[8 * i + 2 * q]) |
+                                       static_cast<uint32_t>(narrow1<XT>(x[8 * i + 2 * q + 1])) << 16;
+                            reinterpret_cast<uint4 *>(op)[i] = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    } else if (live) {
+                        float4 *sp = reinterpret_cast<float4 *>(slot + 2 * kTileRows + int64_t(r) * D + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            sp[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (live) {
+                    if (!whole) {
+                        slot[r] = M;
+                        slot[kTileRows + r] = Lsum;
+                    } else if (a.lse) {
+                        a.lse[int64_t(w.s.row0 + token) * a.heads + head] =
+                            Lsum == 0.f ? -INFINITY : (M + log2f(Lsum)) * 0.6931471805599453f;
+                    }
+                }
+            };
+            if (!split) {
+                output([](int, float x) { return x; });
+            } else {
+                if (t == 1) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        if (own > 0) {
+                            tmem_ld32(o_col + 32 * c, o);
+                            tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            joined[(32 * c + i) * kM + row] = own > 0 ? __uint_as_float(o[i]) * weight * vback : 0.f;
+                    }
+                }
+                join();
+                if (!ok) break;
+                if (t == 0) output([&](int d, float x) { return x + joined[d * kM + row]; });
+                join();  // before the next item's queries
+            }
+            tc_fence_before();
+        }
+    } else if (warp < 8 + kWidenWarps) {
+        // =============================== widening ===============================
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegWiden) : "memory");
+        const int tid = threadIdx.x - 256;
+        constexpr int kN = kRow / 32;          // 16-byte pieces of a thread per tile
+        constexpr int kPieces = kRow / 16;     // of a row
+        uint4 rk[kN], rv[kN];
+        uint32_t zk[kN], zv[kN];
+        int row[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) row[i] = (tid + 256 * i) / kPieces;
+        const int piece = tid % kPieces;
+        uint32_t step_no = 0;
+
+        // loads run one step ahead of stores, page numbers one step ahead of loads
+        int pj = 0, id[kN], kv0 = 0, hi = 0, lo = 0, h = 0;
+        bool have = more;
+        auto fetch_pages = [&]() {  // of the step w, pj
+            kv0 = w.lo + (w.u0 + pj) * kStep;
+            lo = w.s.lo, hi = w.hi, h = w.h;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                int rest;
+                const int pg = page_of_tile(a, (kv0 + row[i]) >> 4, &rest);
+                const bool in = pg < a.b.width && kv0 + (row[i] & ~15) < hi;
+                id[i] = in ? __ldg(a.b.table + w.b * a.b.stride + pg) : -1;
+            }
+        };
+        auto advance = [&]() {
+            if (++pj == w.u1 - w.u0) {
+                pj = 0;
+                more = warp_next(a, &w);
+            }
+            if (more) fetch_pages();
+        };
+        auto load = [&](const uint8_t *codes, const float *scales, uint4 (&r)[kN], uint32_t (&z)[kN]) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int at = kv0 + row[i];
+                r[i] = make_uint4(0, 0, 0, 0);
+                z[i] = 0;
+                if (static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(a.c.pages) && at >= lo && at < hi) {
+                    int rest;
+                    page_of_tile(a, at >> 4, &rest);
+                    const int64_t rr = (int64_t(id[i]) * a.c.heads + h) * a.c.page + rest * 16 + (row[i] & 15);
+                    r[i] = __ldg(reinterpret_cast<const uint4 *>(codes + rr * kRow) + piece);
+                    if (FMT == W4KV_INT4) z[i] = __ldg(reinterpret_cast<const uint32_t *>(scales) + rr) & 15u;
+                }
+            }
+        };
+        auto store = [&](uint8_t *tile, const uint4 (&raw)[kN], const uint32_t (&z)[kN]) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                if (FMT == W4KV_INT4) {
+                    const uint32_t zb = 0x64006400u | z[i] * 0x10001u;
+                    uint8_t *blk = tile + (piece >> 1) * L::kBlock;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {  // the lanes of a phase take different banks
+                        const int j = q ^ ((piece >> 1) * 2);
+                        const uint32_t xx = piece >> 1 ? x[q ^ 2] : x[q];
+                        *reinterpret_cast<uint4 *>(blk + swz(row[i], (piece & 1) * 4 + j)) = widen8_int4(xx, zb);
+                    }
+                } else {
+                    uint8_t *blk = tile + (piece >> 2) * L::kBlock;
+                    const uint2 h0 = widen4<FMT>(x[0]), h1 = widen4<FMT>(x[1]), h2 = widen4<FMT>(x[2]),
+                                h3 = widen4<FMT>(x[3]);
+                    const uint4 c0 = make_uint4(h0.x, h0.y, h1.x, h1.y), c1 = make_uint4(h2.x, h2.y, h3.x, h3.y);
+                    const int c = (piece & 3) * 2, flip = (piece >> 2) & 1;
+                    *reinterpret_cast<uint4 *>(blk + swz(row[i], c + flip)) = flip ? c1 : c0;
+                    *reinterpret_cast<uint4 *>(blk + swz(row[i], c + 1 - flip)) = flip ? c0 : c1;
+                }
+            }
+        };
+        if (have) {
+            fetch_pages();
+            load(a.c.k, a.c.ks, rk, zk);
+            load(a.c.v, a.c.vs, rv, zv);
+            advance();
+        }
+        for (; have; ++step_no) {
+            const int st = step_no % kStages;
+            const uint32_t ph = ((step_no / kStages) & 1) ^ 1;
+            const bool next = more;  // another step: its pages are known
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->k_empty[st]), ph, abort_flag, a.status))) break;
+            store(base + L::kK + st * L::kTile, rk, zk);
+            fence_proxy_async();
+            mbar_arrive(smem_u32(&sm->k_full[st]));
+            if (next) load(a.c.k, a.c.ks, rk, zk);
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->v_empty[st]), ph, abort_flag, a.status))) break;
+            store(base + L::kV + st * L::kTile, rv, zv);
+            fence_proxy_async();
+            mbar_arrive(smem_u32(&sm->v_full[st]));
+            if (next) {
+                load(a.c.v, a.c.vs, rv, zv);
+                advance();
+            }
+            have = next;
+        }
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest) : "memory");
+      if (warp == 16) {
+        // =============================== MMA ===============================
+        if (lane == 0) {
+            constexpr uint32_t id_s = instr_desc<kStep, false>(), id_o = instr_desc<D, true>();
+            const uint32_t q0 = smem_u32(base + L::kQ), k0 = smem_u32(base + L::kK), v0 = smem_u32(base + L::kV);
+            uint32_t step0 = 0, seg_no = 0, n_p[2] = {0, 0};
+            bool ok = true;
+            for (; more && ok; more = next_segment(a, w), ++seg_no) {
+                const bool split = w.R <= kM;
+                const int ns = w.u1 - w.u0, ns_a = stream_steps(a, w, 0);
+                const int slots = split ? ns : 2 * ns;
+                // the stream and step of slot i; slots of a stream past its last step do nothing
+                auto step_of = [&](int i) { return split ? i : i >> 1; };
+                auto live = [&](int i) { return split || (i & 1) || (i >> 1) < ns_a; };
+                auto wait = [&](uint64_t *bar, uint32_t parity) {
+                    ok = ok && mbar_wait(smem_u32(bar), parity, abort_flag, a.status);
+                    return ok;
+                };
+                auto score = [&](int i) {  // S of slot i
+                    const int t = i & 1, j = step_of(i);
+                    const uint32_t no = step0 + j;
+                    const int st = no % kStages;
+                    if (j == (split ? t : 0) && !wait(&sm->q_full[t], seg_no & 1)) return;
+                    if (!live(i)) return;
+                    if (!wait(&sm->k_full[st], (no / kStages) & 1)) return;
+                    tc_fence_after();
+                    const uint32_t q = q0 + t * L::kTile, k = k0 + st * L::kTile;
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        const uint32_t off = (x / 4) * L::kBlock + (x % 4) * 32;
+                        mma_ss(tS + t * kStep, sw128_desc(q + off), sw128_desc(k + off), id_s, x > 0);
+                    }
+                    mma_commit(smem_u32(&sm->s_full[t]));
+                    if (split || t == 1) mma_commit(smem_u32(&sm->k_empty[st]));
+                };
+                auto output = [&](int i) {  // O of slot i
+                    const int t = i & 1, j = step_of(i);
+                    const uint32_t no = step0 + j;
+                    const int st = no % kStages;
+                    if (!live(i)) return;
+                    if (!wait(&sm->p_full[t], n_p[t] & 1)) return;
+                    ++n_p[t];
+                    if (!wait(&sm->v_full[st], (no / kStages) & 1)) return;
+                    tc_fence_after();
+                    const uint32_t v = v0 + st * L::kTile;
+                    const bool first = split ? j == t : j == 0;
+#pragma unroll
+                    for (int x = 0; x < kStep / 16; ++x)
+                        mma_ts(tO + t * 128, tS + t * kStep + 8 * x, mn_desc(v + x * 2048, L::kBlock), id_o,
+                               !(first && x == 0));
+                    mma_commit(smem_u32(&sm->pv_done[t]));
+                    if (split || t == 1) mma_commit(smem_u32(&sm->v_empty[st]));
+                };
+                // a split item of one step still has two query tiles to take in
+                if (ok) score(0);
+                if (ok && slots > 1) score(1);
+                if (ok && slots == 1) wait(&sm->q_full[1], seg_no & 1);
+                for (int i = 0; i < slots && ok; ++i) {
+                    output(i);
+                    if (ok && i + 2 < slots) score(i + 2);
+                }
+                step0 += ns;
+            }
+        }
+        __syncwarp();
+      } else if (warp == 17) {
+        // =============================== scales ===============================
+        int pj = 0, vexp = 7;
+        bool have = more, first = true;
+        uint32_t kw[4], vw[4], badbits = 0;
+        auto load = [&]() {  // words of the step w, pj: tokens lane + 32 i; then on to the next step
+            badbits = 0;
+            first = pj == 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = w.lo + (w.u0 + pj) * kStep + 32 * i + lane;
+                kw[i] = vw[i] = 0;
+                int rest;
+                const int pg = page_of_tile(a, at >> 4, &rest);
+                int id = -1;
+                if (pg < a.b.width && (at & ~15) < w.hi) id = __ldg(a.b.table + w.b * a.b.stride + pg);
+                const bool good = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.c.pages);
+                const uint32_t b = __ballot_sync(0xffffffffu, !good && (at & ~15) < w.hi);
+                if (b & 1u) badbits |= 1u << (2 * i);
+                if (b >> 31) badbits |= 2u << (2 * i);
+                if (good && at >= w.s.lo && at < w.hi) {
+                    const int64_t rr = (int64_t(id) * a.c.heads + w.h) * a.c.page + rest * 16 + (at & 15);
+                    kw[i] = __ldg(reinterpret_cast<const uint32_t *>(a.c.ks) + rr);
+                    vw[i] = __ldg(reinterpret_cast<const uint32_t *>(a.c.vs) + rr);
+                }
+            }
+            if (++pj == w.u1 - w.u0) {
+                pj = 0;
+                more = warp_next(a, &w);
+            }
+        };
+        if (have) load();
+        for (uint32_t step_no = 0; have; ++step_no) {
+            const int sc = step_no % kScaleStages;
+            uint32_t ve = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t e = (vw[i] >> 23) & 255u;
+                ve = max(ve, e == 255u ? 0u : e);
+            }
+            // of the item's part: the streams start anew with each
+            vexp = max(first ? 7 : vexp, static_cast<int>(__reduce_max_sync(0xffffffffu, ve)));
+            const float vmul = pow2i(133 - vexp);
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->sc_empty[sc]),
+                                                   ((step_no / kScaleStages) & 1) ^ 1, abort_flag, a.status)))
+                break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float k = FMT == W4KV_INT4 ? int4_scale(kw[i]) : __uint_as_float(kw[i]);
+                const float v = FMT == W4KV_INT4 ? int4_scale(vw[i]) : __uint_as_float(vw[i]);
+                sm->ks[sc][32 * i + lane] = k * a.scale_log2;
+                sm->vs[sc][32 * i + lane] = v * vmul;
+            }
+            if (lane == 0) {
+                sm->vexp[sc] = vexp;
+                sm->bad[sc] = badbits;
+                if (badbits) atomicOr(a.status, kStatusBounds);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm->sc_full[sc]));
+            have = more;
+            if (have) load();
+        }
+      }
+    }
+    // MMAs in flight are waited for by the softmax warps (pv_done of the last
+    // step); after an abort nothing reads them, and the wait below is bounded.
+    if (*abort_flag && warp == 16 && lane == 0) {
+        const unsigned long long t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 16) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+    }
+}
+
+template <int FMT, int D, int XT>
+int run(const Attn &a, int grid, cudaStream_t stream) {
+    auto kernel = tiled_kernel<FMT, D, XT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
+    if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(tiled_kernel)", e);
+    kernel<<<grid, kThreads, Layout<D>::kSmem, stream>>>(a);
+    return cuda_status(cudaGetLastError());
+}
+
+template <int FMT, int D>
+int run_x(const Attn &a, int xt, int grid, cudaStream_t s) {
+    return xt == W4_F16 ? run<FMT, D, W4_F16>(a, grid, s) : run<FMT, D, W4_BF16>(a, grid, s);
+}
+
+}  // namespace
+
+int launch_tiled_attention(const Attn &a, int fmt, int dim, int xt, int grid, cudaStream_t stream) {
+    if (dim == 64) {
+        if (fmt == W4KV_INT8) return run_x<W4KV_INT8, 64>(a, xt, grid, stream);
+        if (fmt == W4KV_E4M3) return run_x<W4KV_E4M3, 64>(a, xt, grid, stream);
+        return run_x<W4KV_INT4, 64>(a, xt, grid, stream);
+    }
+    if (fmt == W4KV_INT8) return run_x<W4KV_INT8, 128>(a, xt, grid, stream);
+    if (fmt == W4KV_E4M3) return run_x<W4KV_E4M3, 128>(a, xt, grid, stream);
+    return run_x<W4KV_INT4, 128>(a, xt, grid, stream);
+}
+
+}  // namespace kv
+}  // namespace w4
