@@ -19,10 +19,9 @@
 // Warps (18): 0-3 softmax of A (a row per thread), 4-7 of B; 8-15 read codes
 // from the pages (one step ahead, in registers) and widen them into the
 // swizzled operand tiles (K and V, two stages each; V is the MN-major operand,
-// so both have the layout of the rows as they lie); 16 issues the MMAs (one
-// thread); 17 prepares the steps' scales.  The MMA order is S_A(0) S_B(0), then
-// per step O_A, S_A(next), O_B, S_B(next): while one stream's softmax runs the
-// tensor cores work on the other's.
+// so both have the layout of the rows as they lie); 16 and 17 issue the MMAs of
+// A and B; 18 prepares the steps' scales.  A stream's MMAs are S(0), then per
+// step O, S(next): while its softmax runs the tensor cores work on the other's.
 //
 // What bounds it: per step and tile 1024 cycles of tensor cores
 // (2 x 128 x 128 x dim / 4096 a cycle at dim 128), 1024 cycles of exp2 (128 x
@@ -47,8 +46,9 @@ static_assert(kTileRows == 2 * kM, "two tiles");
 constexpr int kStep = kUnit;         // cached tokens per step (MMA N of S, K of P V)
 constexpr int kStages = 2;           // operand stages of K and of V
 constexpr int kScaleStages = 4;
+constexpr int kScaleAhead = 3;       // steps that scale words are copied ahead of use
 constexpr int kWidenWarps = 8;
-constexpr int kThreads = 32 * (8 + kWidenWarps + 4);  // warps 18 and 19 only complete a warpgroup
+constexpr int kThreads = 32 * (8 + kWidenWarps + 4);  // warp 19 only completes a warpgroup
 // Registers per thread: launched with 96 x 640 = 61440, and split into
 // 144 x 256 (softmax) + 72 x 256 (widening) + 48 x 128 = 61440.
 constexpr int kRegSoftmax = 144, kRegWiden = 72, kRegRest = 48;
@@ -164,13 +164,15 @@ __device__ __forceinline__ bool warp_next(const Attn &a, Walk *w) {
 struct alignas(16) Control {
     float ks[kScaleStages][kStep];  // key scales times scale * log2(e)
     float vs[kScaleStages][kStep];  // value scales times 2^(133 - vexp)
+    uint32_t word[kScaleAhead + 1][2][kStep];  // scale words on their way: keys, values
+    uint32_t word_bad[kScaleAhead + 1];        // their bad groups; bit 31: opens a segment
     float stat[2][2][kM];           // [stream][maximum, sum][row], to join split streams
     int vexp[kScaleStages];         // exponent field the value scales are relative to
     uint32_t bad[kScaleStages];     // bit i: tokens 16 i .. 16 i + 15 have no page
     uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t sc_full[kScaleStages], sc_empty[kScaleStages], joined;
-    Walk walk[8 + kWidenWarps + 2];  // of each warp: read by all its lanes, moved by lane 0
+    Walk walk[8 + kWidenWarps + 4];  // of each warp: read by all its lanes, moved by lane 0
     RangeSmem range;
     uint32_t tmem;
     int abort_flag;
@@ -197,33 +199,32 @@ __host__ __device__ constexpr uint32_t instr_desc() {
            (static_cast<uint32_t>(kM >> 4) << 24);
 }
 
-// MN-major operand, 128-byte swizzle: 64 elements of MN per 128-byte row, 8 rows
-// (k) 1024 bytes apart, the next 64 elements `kBlock` bytes on.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t block) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
-    d |= static_cast<uint64_t>(block >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
+// Shared-memory descriptors, 128-byte swizzle, rows of 128 bytes in groups of 8
+// (1024 bytes apart).  The low word holds the address and, for an MN-major
+// operand of more than 64 elements, the distance of the next 64 (leading byte
+// offset); the high word is the same for all: stride offset, version, swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t leading) {
+    return ((saddr & 0x3FFFF) >> 4) | (leading >> 4) << 16;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(kDescHigh)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_low), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(kDescHigh)
         : "memory");
 }
 
@@ -269,6 +270,14 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) 
 
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 // Pairs of fp32 in one 64-bit register.
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                                 ~static_cast<uintptr_t>(1023));
     Control *sm = reinterpret_cast<Control *>(base + L::kControl);
     volatile int *abort_flag = &sm->abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
@@ -356,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sm->k_full[i]), 32 * kWidenWarps);
-            mbar_init(smem_u32(&sm->k_empty[i]), 1);
+            mbar_init(smem_u32(&sm->k_empty[i]), 2);  // both streams
             mbar_init(smem_u32(&sm->v_full[i]), 32 * kWidenWarps);
-            mbar_init(smem_u32(&sm->v_empty[i]), 1);
+            mbar_init(smem_u32(&sm->v_empty[i]), 2);
         }
         for (int i = 0; i < kScaleStages; ++i) {
             mbar_init(smem_u32(&sm->sc_full[i]), 1);
@@ -390,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
     const uint32_t tmem = sm->tmem;
     const uint32_t tS = tmem, tO = tmem + 2 * kStep;  // + 128 t
 
-    Walk &w = sm->walk[min(warp, 8 + kWidenWarps + 1)];
-    bool more = false;
-    if (warp < 8 + kWidenWarps + 2) {
+    Walk &w = sm->walk[warp];
+    bool more;
+    {
         int first = 0;
         if (lane == 0) first = first_segment(a, range, w);
         more = __shfl_sync(0xffffffffu, first, 0) != 0;
@@ -819,113 +828,148 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         }
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest) : "memory");
-      if (warp == 16) {
+      if (warp < 18) {
         // =============================== MMA ===============================
-        if (lane == 0) {
-            constexpr uint32_t id_s = instr_desc<kStep, false>(), id_o = instr_desc<D, true>();
-            const uint32_t q0 = smem_u32(base + L::kQ), k0 = smem_u32(base + L::kK), v0 = smem_u32(base + L::kV);
-            uint32_t step0 = 0, seg_no = 0, n_p[2] = {0, 0};
-            bool ok = true;
-            for (; more && ok; more = next_segment(a, w), ++seg_no) {
-                const bool split = w.R <= kM;
-                const int ns = w.u1 - w.u0, ns_a = stream_steps(a, w, 0);
-                const int slots = split ? ns : 2 * ns;
-                // the stream and step of slot i; slots of a stream past its last step do nothing
-                auto step_of = [&](int i) { return split ? i : i >> 1; };
-                auto live = [&](int i) { return split || (i & 1) || (i >> 1) < ns_a; };
-                auto wait = [&](uint64_t *bar, uint32_t parity) {
-                    ok = ok && mbar_wait(smem_u32(bar), parity, abort_flag, a.status);
-                    return ok;
-                };
-                auto score = [&](int i) {  // S of slot i
-                    const int t = i & 1, j = step_of(i);
-                    const uint32_t no = step0 + j;
+        // One warp per stream, so that the waits and commits of one (100 cycles
+        // and more each) pass while the other's MMAs run.  The whole warp walks,
+        // one elected thread issues.
+        const int t = warp - 16;
+        constexpr uint32_t id_s = instr_desc<kStep, false>(), id_o = instr_desc<D, true>();
+        const uint32_t q = desc_low(smem_u32(base + L::kQ + t * L::kTile), 16);
+        const uint32_t k0 = desc_low(smem_u32(base + L::kK), 16);
+        const uint32_t v0 = desc_low(smem_u32(base + L::kV), L::kBlock);
+        const uint32_t d_s = tS + t * kStep, d_o = tO + t * 128;
+        uint32_t step0 = 0, seg_no = 0, n_p = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(bar), parity, abort_flag, a.status));
+            return ok;
+        };
+        for (; more && ok; more = warp_next(a, &w), ++seg_no) {
+            const bool split = w.R <= kM;
+            const int ns = w.u1 - w.u0, mine = stream_steps(a, w, t);
+            auto own = [&](int j) { return split ? (j & 1) == t : j < mine; };
+            int kj = 0;  // step whose keys are taken next
+            auto score = [&]() {  // S of the next step of the stream; keys of the others' steps are let go
+                for (; kj < ns && ok; ++kj) {
+                    const uint32_t no = step0 + kj;
                     const int st = no % kStages;
-                    if (j == (split ? t : 0) && !wait(&sm->q_full[t], seg_no & 1)) return;
-                    if (!live(i)) return;
                     if (!wait(&sm->k_full[st], (no / kStages) & 1)) return;
-                    tc_fence_after();
-                    const uint32_t q = q0 + t * L::kTile, k = k0 + st * L::kTile;
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t off = (x / 4) * L::kBlock + (x % 4) * 32;
-                        mma_ss(tS + t * kStep, sw128_desc(q + off), sw128_desc(k + off), id_s, x > 0);
+                    if (!own(kj)) {
+                        if (lane == 0) mbar_arrive(smem_u32(&sm->k_empty[st]));
+                        continue;
                     }
-                    mma_commit(smem_u32(&sm->s_full[t]));
-                    if (split || t == 1) mma_commit(smem_u32(&sm->k_empty[st]));
-                };
-                auto output = [&](int i) {  // O of slot i
-                    const int t = i & 1, j = step_of(i);
-                    const uint32_t no = step0 + j;
-                    const int st = no % kStages;
-                    if (!live(i)) return;
-                    if (!wait(&sm->p_full[t], n_p[t] & 1)) return;
-                    ++n_p[t];
-                    if (!wait(&sm->v_full[st], (no / kStages) & 1)) return;
                     tc_fence_after();
-                    const uint32_t v = v0 + st * L::kTile;
-                    const bool first = split ? j == t : j == 0;
+                    if (elect_one()) {
+                        const uint32_t k = k0 + st * (L::kTile >> 4);
+#pragma unroll
+                        for (int x = 0; x < D / 16; ++x) {
+                            const uint32_t off = ((x / 4) * L::kBlock + (x % 4) * 32) >> 4;
+                            mma_ss(d_s, q + off, k + off, id_s, x > 0);
+                        }
+                        mma_commit(smem_u32(&sm->s_full[t]));
+                        mma_commit(smem_u32(&sm->k_empty[st]));
+                    }
+                    __syncwarp();
+                    ++kj;
+                    return;
+                }
+            };
+            if (!wait(&sm->q_full[t], seg_no & 1)) break;
+            score();
+            bool first = true;
+            for (int j = 0; j < ns && ok; ++j) {  // O of each step of the stream
+                const uint32_t no = step0 + j;
+                const int st = no % kStages;
+                if (own(j) && !wait(&sm->p_full[t], n_p++ & 1)) break;
+                if (!wait(&sm->v_full[st], (no / kStages) & 1)) break;
+                if (!own(j)) {
+                    if (lane == 0) mbar_arrive(smem_u32(&sm->v_empty[st]));
+                    continue;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t v = v0 + st * (L::kTile >> 4);
 #pragma unroll
                     for (int x = 0; x < kStep / 16; ++x)
-                        mma_ts(tO + t * 128, tS + t * kStep + 8 * x, mn_desc(v + x * 2048, L::kBlock), id_o,
-                               !(first && x == 0));
+                        mma_ts(d_o, d_s + 8 * x, v + x * (2048 >> 4), id_o, !(first && x == 0));
                     mma_commit(smem_u32(&sm->pv_done[t]));
-                    if (split || t == 1) mma_commit(smem_u32(&sm->v_empty[st]));
-                };
-                // a split item of one step still has two query tiles to take in
-                if (ok) score(0);
-                if (ok && slots > 1) score(1);
-                if (ok && slots == 1) wait(&sm->q_full[1], seg_no & 1);
-                for (int i = 0; i < slots && ok; ++i) {
-                    output(i);
-                    if (ok && i + 2 < slots) score(i + 2);
+                    mma_commit(smem_u32(&sm->v_empty[st]));
                 }
-                step0 += ns;
+                __syncwarp();
+                first = false;
+                score();
             }
+            // keys of steps behind the stream's last one
+            while (kj < ns && ok) score();
+            step0 += ns;
         }
-        __syncwarp();
-      } else if (warp == 17) {
+      } else if (warp == 18) {
         // =============================== scales ===============================
-        int pj = 0, vexp = 7;
-        bool have = more, first = true;
-        uint32_t kw[4], vw[4], badbits = 0;
-        auto load = [&]() {  // words of the step w, pj: tokens lane + 32 i; then on to the next step
-            badbits = 0;
-            first = pj == 0;
+        // Page numbers are read one step before the words' copies are issued, and
+        // those (cp.async, each lane its own words) kScaleAhead steps before use.
+        int pj = 0, kv0 = 0, lo = 0, hi = 0, h = 0, id[4], vexp = 7;
+        bool fetched = more, opens = false;  // a step's page numbers are at hand; it opens a segment
+        uint32_t issued = 0;
+        auto fetch_pages = [&]() {
+            kv0 = w.lo + (w.u0 + pj) * kStep, lo = w.s.lo, hi = w.hi, h = w.h;
+            opens = pj == 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int at = w.lo + (w.u0 + pj) * kStep + 32 * i + lane;
-                kw[i] = vw[i] = 0;
+                const int tile = (kv0 + 32 * i + lane) >> 4;
                 int rest;
-                const int pg = page_of_tile(a, at >> 4, &rest);
-                int id = -1;
-                if (pg < a.b.width && (at & ~15) < w.hi) id = __ldg(a.b.table + w.b * a.b.stride + pg);
-                const bool good = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.c.pages);
-                const uint32_t b = __ballot_sync(0xffffffffu, !good && (at & ~15) < w.hi);
-                if (b & 1u) badbits |= 1u << (2 * i);
-                if (b >> 31) badbits |= 2u << (2 * i);
-                if (good && at >= w.s.lo && at < w.hi) {
-                    const int64_t rr = (int64_t(id) * a.c.heads + w.h) * a.c.page + rest * 16 + (at & 15);
-                    kw[i] = __ldg(reinterpret_cast<const uint32_t *>(a.c.ks) + rr);
-                    vw[i] = __ldg(reinterpret_cast<const uint32_t *>(a.c.vs) + rr);
-                }
+                const int pg = page_of_tile(a, tile, &rest);
+                id[i] = pg < a.b.width && tile * 16 < hi ? __ldg(a.b.table + w.b * a.b.stride + pg) : -1;
             }
             if (++pj == w.u1 - w.u0) {
                 pj = 0;
                 more = warp_next(a, &w);
             }
         };
-        if (have) load();
-        for (uint32_t step_no = 0; have; ++step_no) {
-            const int sc = step_no % kScaleStages;
-            uint32_t ve = 0;
+        auto issue = [&]() {
+            if (fetched) {
+                const int rs = issued++ % (kScaleAhead + 1);
+                uint32_t badbits = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = kv0 + 32 * i + lane;
+                    int rest;
+                    page_of_tile(a, at >> 4, &rest);
+                    const bool good = static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(a.c.pages);
+                    const uint32_t b = __ballot_sync(0xffffffffu, !good && (at & ~15) < hi);
+                    badbits |= ((b & 1u) | (b >> 31 << 1)) << (2 * i);
+                    const int n = good && at >= lo && at < hi ? 4 : 0;  // else a word of zeros
+                    const int64_t rr = n ? (int64_t(id[i]) * a.c.heads + h) * a.c.page + rest * 16 + (at & 15) : 0;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                     smem_u32(&sm->word[rs][0][32 * i + lane])), "l"(a.c.ks + rr), "r"(n) : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                     smem_u32(&sm->word[rs][1][32 * i + lane])), "l"(a.c.vs + rr), "r"(n) : "memory");
+                }
+                if (lane == 0) sm->word_bad[rs] = badbits | (opens ? 1u << 31 : 0u);
+                fetched = more;
+                if (fetched) fetch_pages();
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        if (fetched) fetch_pages();
+        for (int i = 0; i < kScaleAhead; ++i) issue();
+        for (uint32_t step_no = 0;; ++step_no) {
+            issue();
+            if (step_no == issued) break;  // all steps are done
+            const int sc = step_no % kScaleStages, rs = step_no % (kScaleAhead + 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kScaleAhead) : "memory");
+            __syncwarp();
+            const uint32_t info = sm->word_bad[rs];
+            uint32_t kw[4], vw[4], ve = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                kw[i] = sm->word[rs][0][32 * i + lane];
+                vw[i] = sm->word[rs][1][32 * i + lane];
                 const uint32_t e = (vw[i] >> 23) & 255u;
                 ve = max(ve, e == 255u ? 0u : e);
             }
             // of the item's part: the streams start anew with each
-            vexp = max(first ? 7 : vexp, static_cast<int>(__reduce_max_sync(0xffffffffu, ve)));
+            vexp = max(info >> 31 ? 7 : vexp, static_cast<int>(__reduce_max_sync(0xffffffffu, ve)));
             const float vmul = pow2i(133 - vexp);
             if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->sc_empty[sc]),
                                                    ((step_no / kScaleStages) & 1) ^ 1, abort_flag, a.status)))
@@ -939,14 +983,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             }
             if (lane == 0) {
                 sm->vexp[sc] = vexp;
-                sm->bad[sc] = badbits;
-                if (badbits) atomicOr(a.status, kStatusBounds);
+                sm->bad[sc] = info & 255u;
+                if (info & 255u) atomicOr(a.status, kStatusBounds);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm->sc_full[sc]));
-            have = more;
-            if (have) load();
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
       }
     }
     // MMAs in flight are waited for by the softmax warps (pv_done of the last
