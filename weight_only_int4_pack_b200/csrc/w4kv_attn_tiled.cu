@@ -17,8 +17,8 @@
 // that the tensor cores and the softmax still alternate.
 //
 // Warps (18): 0-3 softmax of A (a row per thread), 4-7 of B; 8-15 read codes
-// from the pages (one step ahead, in registers) and widen them into the
-// swizzled operand tiles (K and V, two stages each; V is the MN-major operand,
+// from the pages (copied some tiles ahead) and widen them into the swizzled
+// operand tiles (three buffers for K and V in turn; V is the MN-major operand,
 // so both have the layout of the rows as they lie); 16 and 17 issue the MMAs of
 // A and B; 18 prepares the steps' scales.  A stream's MMAs are S(0), then per
 // step O, S(next): while its softmax runs the tensor cores work on the other's.
@@ -44,14 +44,14 @@ constexpr int kM = 128;              // rows of a tile (MMA M, TMEM lanes)
 constexpr int kTileRows = kTiledRows;  // rows of an item
 static_assert(kTileRows == 2 * kM, "two tiles");
 constexpr int kStep = kUnit;         // cached tokens per step (MMA N of S, K of P V)
-constexpr int kStages = 2;           // operand stages of K and of V
+constexpr int kBuffers = 3;          // operand buffers, taken by K(0) V(0) K(1) V(1) .. in turn
 constexpr int kScaleStages = 4;
 constexpr int kScaleAhead = 3;       // steps that scale words are copied ahead of use
 constexpr int kWidenWarps = 8;
 constexpr int kThreads = 32 * (8 + kWidenWarps + 4);  // warp 19 only completes a warpgroup
 // Registers per thread: launched with 96 x 640 = 61440, and split into
-// 144 x 256 (softmax) + 72 x 256 (widening) + 48 x 128 = 61440.
-constexpr int kRegSoftmax = 144, kRegWiden = 72, kRegRest = 48;
+// 152 x 256 (softmax) + 64 x 256 (widening) + 48 x 128 = 61440.
+constexpr int kRegSoftmax = 152, kRegWiden = 64, kRegRest = 48;
 static_assert(kRegSoftmax * 256 + kRegWiden * 256 + kRegRest * 128 <= 96 * kThreads, "register split");
 constexpr int kTmemCols = 512;
 
@@ -170,7 +170,7 @@ struct alignas(16) Control {
     int vexp[kScaleStages];         // exponent field the value scales are relative to
     uint32_t bad[kScaleStages];     // bit i: tokens 16 i .. 16 i + 15 have no page
     uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
-    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t full[kBuffers], empty[kBuffers];
     uint64_t sc_full[kScaleStages], sc_empty[kScaleStages], joined;
     Walk walk[8 + kWidenWarps + 4];  // of each warp: read by all its lanes, moved by lane 0
     RangeSmem range;
@@ -178,16 +178,22 @@ struct alignas(16) Control {
     int abort_flag;
 };
 
-template <int D>
+template <int FMT, int D>
 struct Layout {
-    static constexpr int kBlock = 128 * 128;  // 128 rows of 64 fp16: the swizzled unit
+    static constexpr int kRow = FMT == W4KV_INT4 ? D / 2 : D;  // code bytes of a row
+    static constexpr int kBlock = 128 * 128;                   // 128 rows of 64 fp16: the swizzled unit
     static constexpr int kBlocks = D / 64;
     static constexpr int kTile = kBlocks * kBlock;
-    static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile;
-    static constexpr int kControl = kV + kStages * kTile;
+    // codes (and for INT4 their rows' scale words) on their way, lane by lane
+    static constexpr int kPieces = kStep * kRow / 16 / (32 * kWidenWarps);  // 16-byte pieces of a thread
+    static constexpr int kRawTile = kPieces * 32 * kWidenWarps * (FMT == W4KV_INT4 ? 20 : 16);
+    static constexpr int kRawTiles = kRow == 128 ? 3 : 5;
+    static constexpr int kQ = 0, kKV = 2 * kTile, kRaw = kKV + kBuffers * kTile;
+    static constexpr int kControl = kRaw + kRawTiles * kRawTile;
     // at least 120 KB, so that one block (all of tensor memory) is on an SM
     static constexpr int kUsed = kControl + static_cast<int>(sizeof(Control)) + 1024;
     static constexpr int kSmem = kUsed < 120 * 1024 ? 120 * 1024 : kUsed;
+    static_assert(kSmem <= 227 * 1024 && kControl % 16 == 0, "shared memory");
 };
 
 // ---- instructions ------------------------------------------------------------------------------
@@ -346,8 +352,8 @@ __device__ __forceinline__ uint4 widen8_int4(uint32_t w, uint32_t zb) {
 
 template <int FMT, int D, int XT>
 __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
-    using L = Layout<D>;
-    constexpr int kRow = FMT == W4KV_INT4 ? D / 2 : D;  // code bytes of a row
+    using L = Layout<FMT, D>;
+    constexpr int kRow = L::kRow;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -363,11 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             mbar_init(smem_u32(&sm->p_full[t]), kM);
             mbar_init(smem_u32(&sm->pv_done[t]), 1);
         }
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sm->k_full[i]), 32 * kWidenWarps);
-            mbar_init(smem_u32(&sm->k_empty[i]), 2);  // both streams
-            mbar_init(smem_u32(&sm->v_full[i]), 32 * kWidenWarps);
-            mbar_init(smem_u32(&sm->v_empty[i]), 2);
+        for (int i = 0; i < kBuffers; ++i) {
+            mbar_init(smem_u32(&sm->full[i]), 32 * kWidenWarps);
+            mbar_init(smem_u32(&sm->empty[i]), 2);  // both streams
         }
         for (int i = 0; i < kScaleStages; ++i) {
             mbar_init(smem_u32(&sm->sc_full[i]), 1);
@@ -731,64 +735,72 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         // =============================== widening ===============================
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegWiden) : "memory");
         const int tid = threadIdx.x - 256;
-        constexpr int kN = kRow / 32;          // 16-byte pieces of a thread per tile
-        constexpr int kPieces = kRow / 16;     // of a row
-        uint4 rk[kN], rv[kN];
-        uint32_t zk[kN], zv[kN];
-        int row[kN];
-#pragma unroll
-        for (int i = 0; i < kN; ++i) row[i] = (tid + 256 * i) / kPieces;
-        const int piece = tid % kPieces;
-        uint32_t step_no = 0;
-
-        // loads run one step ahead of stores, page numbers one step ahead of loads
+        // A thread copies (cp.async) its own pieces of the codes into its own slots,
+        // kRawTiles tiles ahead, and page numbers are read one step before that.
+        constexpr int kN = L::kPieces;
+        constexpr int kRowPieces = kRow / 16;
+        const int piece = tid % kRowPieces, row0 = tid / kRowPieces;
+        constexpr int kRowStep = 32 * kWidenWarps / kRowPieces;  // rows between a thread's pieces
         int pj = 0, id[kN], kv0 = 0, hi = 0, lo = 0, h = 0;
-        bool have = more;
-        auto fetch_pages = [&]() {  // of the step w, pj
+        bool fetched = more;  // a step's page numbers are at hand
+        auto fetch_pages = [&]() {
             kv0 = w.lo + (w.u0 + pj) * kStep;
             lo = w.s.lo, hi = w.hi, h = w.h;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
+                const int tile = (kv0 + row0 + i * kRowStep) >> 4;
                 int rest;
-                const int pg = page_of_tile(a, (kv0 + row[i]) >> 4, &rest);
-                const bool in = pg < a.b.width && kv0 + (row[i] & ~15) < hi;
-                id[i] = in ? __ldg(a.b.table + w.b * a.b.stride + pg) : -1;
+                const int pg = page_of_tile(a, tile, &rest);
+                id[i] = pg < a.b.width && tile * 16 < hi ? __ldg(a.b.table + w.b * a.b.stride + pg) : -1;
             }
-        };
-        auto advance = [&]() {
             if (++pj == w.u1 - w.u0) {
                 pj = 0;
                 more = warp_next(a, &w);
             }
-            if (more) fetch_pages();
         };
-        auto load = [&](const uint8_t *codes, const float *scales, uint4 (&r)[kN], uint32_t (&z)[kN]) {
+        uint32_t issued = 0;  // tiles
+        int put = 0;
+        auto issue = [&]() {  // the next tile: K of a step, then its V
+            if (fetched) {
+                const bool is_v = issued & 1;
+                const uint32_t dst = smem_u32(base + L::kRaw + put * L::kRawTile) + tid * 16;
+                const uint8_t *codes = (is_v ? a.c.v : a.c.k) + piece * 16;
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const int at = kv0 + row[i];
-                r[i] = make_uint4(0, 0, 0, 0);
-                z[i] = 0;
-                if (static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(a.c.pages) && at >= lo && at < hi) {
+                for (int i = 0; i < kN; ++i) {
+                    const int at = kv0 + row0 + i * kRowStep;
                     int rest;
                     page_of_tile(a, at >> 4, &rest);
-                    const int64_t rr = (int64_t(id[i]) * a.c.heads + h) * a.c.page + rest * 16 + (row[i] & 15);
-                    r[i] = __ldg(reinterpret_cast<const uint4 *>(codes + rr * kRow) + piece);
-                    if (FMT == W4KV_INT4) z[i] = __ldg(reinterpret_cast<const uint32_t *>(scales) + rr) & 15u;
+                    const bool live = static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(a.c.pages) && at >= lo && at < hi;
+                    const int64_t rr = live ? (int64_t(id[i]) * a.c.heads + h) * a.c.page + rest * 16 + (at & 15) : 0;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512 * kWidenWarps),
+                                 "l"(codes + rr * kRow), "r"(live ? 16 : 0) : "memory");
+                    if (FMT == W4KV_INT4)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                         dst - tid * 12 + (kN * 16 + i * 4) * 32 * kWidenWarps),
+                                     "l"((is_v ? a.c.vs : a.c.ks) + rr), "r"(live ? 4 : 0) : "memory");
+                }
+                ++issued;
+                if (is_v) {
+                    fetched = more;
+                    if (fetched) fetch_pages();
                 }
             }
+            put = put + 1 == L::kRawTiles ? 0 : put + 1;
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
         auto store = [&](uint8_t *tile, const uint4 (&raw)[kN], const uint32_t (&z)[kN]) {
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                const int row = row0 + i * kRowStep;
                 if (FMT == W4KV_INT4) {
-                    const uint32_t zb = 0x64006400u | z[i] * 0x10001u;
+                    const uint32_t zb = 0x64006400u | (z[i] & 15u) * 0x10001u;
                     uint8_t *blk = tile + (piece >> 1) * L::kBlock;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {  // the lanes of a phase take different banks
                         const int j = q ^ ((piece >> 1) * 2);
                         const uint32_t xx = piece >> 1 ? x[q ^ 2] : x[q];
-                        *reinterpret_cast<uint4 *>(blk + swz(row[i], (piece & 1) * 4 + j)) = widen8_int4(xx, zb);
+                        *reinterpret_cast<uint4 *>(blk + swz(row, (piece & 1) * 4 + j)) = widen8_int4(xx, zb);
                     }
                 } else {
                     uint8_t *blk = tile + (piece >> 2) * L::kBlock;
@@ -796,36 +808,34 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                 h3 = widen4<FMT>(x[3]);
                     const uint4 c0 = make_uint4(h0.x, h0.y, h1.x, h1.y), c1 = make_uint4(h2.x, h2.y, h3.x, h3.y);
                     const int c = (piece & 3) * 2, flip = (piece >> 2) & 1;
-                    *reinterpret_cast<uint4 *>(blk + swz(row[i], c + flip)) = flip ? c1 : c0;
-                    *reinterpret_cast<uint4 *>(blk + swz(row[i], c + 1 - flip)) = flip ? c0 : c1;
+                    *reinterpret_cast<uint4 *>(blk + swz(row, c + flip)) = flip ? c1 : c0;
+                    *reinterpret_cast<uint4 *>(blk + swz(row, c + 1 - flip)) = flip ? c0 : c1;
                 }
             }
         };
-        if (have) {
-            fetch_pages();
-            load(a.c.k, a.c.ks, rk, zk);
-            load(a.c.v, a.c.vs, rv, zv);
-            advance();
-        }
-        for (; have; ++step_no) {
-            const int st = step_no % kStages;
-            const uint32_t ph = ((step_no / kStages) & 1) ^ 1;
-            const bool next = more;  // another step: its pages are known
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->k_empty[st]), ph, abort_flag, a.status))) break;
-            store(base + L::kK + st * L::kTile, rk, zk);
-            fence_proxy_async();
-            mbar_arrive(smem_u32(&sm->k_full[st]));
-            if (next) load(a.c.k, a.c.ks, rk, zk);
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->v_empty[st]), ph, abort_flag, a.status))) break;
-            store(base + L::kV + st * L::kTile, rv, zv);
-            fence_proxy_async();
-            mbar_arrive(smem_u32(&sm->v_full[st]));
-            if (next) {
-                load(a.c.v, a.c.vs, rv, zv);
-                advance();
+        if (fetched) fetch_pages();
+        for (int i = 0; i < L::kRawTiles; ++i) issue();
+        int get = 0;
+        for (uint32_t n = 0; n < issued; ++n) {
+            const uint32_t buf = n % kBuffers;
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::kRawTiles - 1) : "memory");
+            const uint8_t *src = base + L::kRaw + get * L::kRawTile;
+            uint4 raw[kN];
+            uint32_t z[kN];
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                raw[i] = *reinterpret_cast<const uint4 *>(src + tid * 16 + i * 512 * kWidenWarps);
+                z[i] = FMT == W4KV_INT4 ? *reinterpret_cast<const uint32_t *>(src + tid * 4 + (kN * 16 + i * 4) * 32 * kWidenWarps) : 0u;
             }
-            have = next;
+            get = get + 1 == L::kRawTiles ? 0 : get + 1;
+            issue();
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->empty[buf]), ((n / kBuffers) & 1) ^ 1, abort_flag, a.status)))
+                break;
+            store(base + L::kKV + buf * L::kTile, raw, z);
+            fence_proxy_async();
+            mbar_arrive(smem_u32(&sm->full[buf]));
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest) : "memory");
       if (warp < 18) {
@@ -836,8 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         const int t = warp - 16;
         constexpr uint32_t id_s = instr_desc<kStep, false>(), id_o = instr_desc<D, true>();
         const uint32_t q = desc_low(smem_u32(base + L::kQ + t * L::kTile), 16);
-        const uint32_t k0 = desc_low(smem_u32(base + L::kK), 16);
-        const uint32_t v0 = desc_low(smem_u32(base + L::kV), L::kBlock);
+        const uint32_t k0 = desc_low(smem_u32(base + L::kKV), 16);
+        const uint32_t v0 = desc_low(smem_u32(base + L::kKV), L::kBlock);
         const uint32_t d_s = tS + t * kStep, d_o = tO + t * 128;
         uint32_t step0 = 0, seg_no = 0, n_p = 0;
         bool ok = true;
@@ -848,60 +858,48 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         for (; more && ok; more = warp_next(a, &w), ++seg_no) {
             const bool split = w.R <= kM;
             const int ns = w.u1 - w.u0, mine = stream_steps(a, w, t);
-            auto own = [&](int j) { return split ? (j & 1) == t : j < mine; };
-            int kj = 0;  // step whose keys are taken next
-            auto score = [&]() {  // S of the next step of the stream; keys of the others' steps are let go
-                for (; kj < ns && ok; ++kj) {
-                    const uint32_t no = step0 + kj;
-                    const int st = no % kStages;
-                    if (!wait(&sm->k_full[st], (no / kStages) & 1)) return;
-                    if (!own(kj)) {
-                        if (lane == 0) mbar_arrive(smem_u32(&sm->k_empty[st]));
-                        continue;
-                    }
+            if (!wait(&sm->q_full[t], seg_no & 1)) break;
+            // Tiles are taken, or let go, in the order they are widened.
+            bool first = true;
+            for (int j = 0; j < ns && ok; ++j) {
+                const bool own = split ? (j & 1) == t : j < mine;
+                const uint32_t kn = 2 * (step0 + j), vn = kn + 1;
+                const uint32_t kb = kn % kBuffers, vb = vn % kBuffers;
+                if (!wait(&sm->full[kb], (kn / kBuffers) & 1)) break;
+                if (!own) {
+                    if (lane == 0) mbar_arrive(smem_u32(&sm->empty[kb]));
+                } else {
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t k = k0 + st * (L::kTile >> 4);
+                        const uint32_t k = k0 + kb * (L::kTile >> 4);
 #pragma unroll
                         for (int x = 0; x < D / 16; ++x) {
                             const uint32_t off = ((x / 4) * L::kBlock + (x % 4) * 32) >> 4;
                             mma_ss(d_s, q + off, k + off, id_s, x > 0);
                         }
                         mma_commit(smem_u32(&sm->s_full[t]));
-                        mma_commit(smem_u32(&sm->k_empty[st]));
+                        mma_commit(smem_u32(&sm->empty[kb]));
                     }
                     __syncwarp();
-                    ++kj;
-                    return;
+                    if (!wait(&sm->p_full[t], n_p++ & 1)) break;
                 }
-            };
-            if (!wait(&sm->q_full[t], seg_no & 1)) break;
-            score();
-            bool first = true;
-            for (int j = 0; j < ns && ok; ++j) {  // O of each step of the stream
-                const uint32_t no = step0 + j;
-                const int st = no % kStages;
-                if (own(j) && !wait(&sm->p_full[t], n_p++ & 1)) break;
-                if (!wait(&sm->v_full[st], (no / kStages) & 1)) break;
-                if (!own(j)) {
-                    if (lane == 0) mbar_arrive(smem_u32(&sm->v_empty[st]));
-                    continue;
-                }
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t v = v0 + st * (L::kTile >> 4);
+                if (!wait(&sm->full[vb], (vn / kBuffers) & 1)) break;
+                if (!own) {
+                    if (lane == 0) mbar_arrive(smem_u32(&sm->empty[vb]));
+                } else {
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t v = v0 + vb * (L::kTile >> 4);
 #pragma unroll
-                    for (int x = 0; x < kStep / 16; ++x)
-                        mma_ts(d_o, d_s + 8 * x, v + x * (2048 >> 4), id_o, !(first && x == 0));
-                    mma_commit(smem_u32(&sm->pv_done[t]));
-                    mma_commit(smem_u32(&sm->v_empty[st]));
+                        for (int x = 0; x < kStep / 16; ++x)
+                            mma_ts(d_o, d_s + 8 * x, v + x * (2048 >> 4), id_o, !(first && x == 0));
+                        mma_commit(smem_u32(&sm->pv_done[t]));
+                        mma_commit(smem_u32(&sm->empty[vb]));
+                    }
+                    __syncwarp();
+                    first = false;
                 }
-                __syncwarp();
-                first = false;
-                score();
             }
-            // keys of steps behind the stream's last one
-            while (kj < ns && ok) score();
             step0 += ns;
         }
       } else if (warp == 18) {
@@ -1011,9 +1009,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
 template <int FMT, int D, int XT>
 int run(const Attn &a, int grid, cudaStream_t stream) {
     auto kernel = tiled_kernel<FMT, D, XT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<FMT, D>::kSmem);
     if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(tiled_kernel)", e);
-    kernel<<<grid, kThreads, Layout<D>::kSmem, stream>>>(a);
+    kernel<<<grid, kThreads, Layout<FMT, D>::kSmem, stream>>>(a);
     return cuda_status(cudaGetLastError());
 }
 
