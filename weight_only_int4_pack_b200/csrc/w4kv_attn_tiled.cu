@@ -50,8 +50,8 @@ constexpr int kScaleAhead = 3;       // steps that scale words are copied ahead 
 constexpr int kWidenWarps = 8;
 constexpr int kThreads = 32 * (8 + kWidenWarps + 4);  // warp 19 only completes a warpgroup
 // Registers per thread: launched with 96 x 640 = 61440, and split into
-// 152 x 256 (softmax) + 64 x 256 (widening) + 48 x 128 = 61440.
-constexpr int kRegSoftmax = 152, kRegWiden = 64, kRegRest = 48;
+// 160 x 256 (softmax) + 56 x 256 (widening) + 48 x 128 = 61440.
+constexpr int kRegSoftmax = 160, kRegWiden = 56, kRegRest = 48;
 static_assert(kRegSoftmax * 256 + kRegWiden * 256 + kRegRest * 128 <= 96 * kThreads, "register split");
 constexpr int kTmemCols = 512;
 
@@ -184,9 +184,9 @@ struct Layout {
     static constexpr int kBlock = 128 * 128;                   // 128 rows of 64 fp16: the swizzled unit
     static constexpr int kBlocks = D / 64;
     static constexpr int kTile = kBlocks * kBlock;
-    // codes (and for INT4 their rows' scale words) on their way, lane by lane
-    static constexpr int kPieces = kStep * kRow / 16 / (32 * kWidenWarps);  // 16-byte pieces of a thread
-    static constexpr int kRawTile = kPieces * 32 * kWidenWarps * (FMT == W4KV_INT4 ? 20 : 16);
+    // Codes on their way: a warp's 16 rows of a tile, and for INT4 their scale words.
+    static constexpr int kRawWarp = 16 * kRow + (FMT == W4KV_INT4 ? 64 : 0);
+    static constexpr int kRawTile = kWidenWarps * kRawWarp;
     static constexpr int kRawTiles = kRow == 128 ? 3 : 5;
     static constexpr int kQ = 0, kKV = 2 * kTile, kRaw = kKV + kBuffers * kTile;
     static constexpr int kControl = kRaw + kRawTiles * kRawTile;
@@ -197,6 +197,34 @@ struct Layout {
 };
 
 // ---- instructions ------------------------------------------------------------------------------
+
+// Bounded wait (kWaitNs), with the thread suspended between looks at the clock
+// and the abort flag, so that waiting warps take no issue slots.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                         unsigned *status) {
+    auto attempt = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    if (attempt()) return true;
+    const unsigned long long t0 = globaltimer();
+    while (!attempt()) {
+        if (*abort_flag) return false;
+        if (globaltimer() - t0 > kWaitNs) {
+            *abort_flag = 1;
+            atomicOr(status, 1u);
+            return false;
+        }
+    }
+    return true;
+}
 
 // kind::f16, D f32, A and B fp16, M = 128; kTransB: B is MN-major.
 template <int N, bool kTransB>
@@ -268,10 +296,33 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
         : "r"(addr));
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
+}
+
+// Waits for the loads issued so far; r depends on it.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                   "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st() {
@@ -422,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         bool ok = true;
         auto join = [&]() {  // both streams' warps, bounded like every wait
             mbar_arrive(smem_u32(&sm->joined));
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->joined), joins & 1, abort_flag, a.status));
+            ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&sm->joined), joins & 1, abort_flag, a.status));
             ++joins;
         };
         for (; more && ok; more = warp_next(a, &w)) {
@@ -483,11 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             const int ns = w.u1 - w.u0, mine = stream_steps(a, w, t), kv_base = w.lo + w.u0 * kStep;
             for (int j = 0; j < ns && ok; ++j, ++step_no) {
                 const int sc = step_no % kScaleStages;
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->sc_full[sc]),
+                ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&sm->sc_full[sc]),
                                                        (step_no / kScaleStages) & 1, abort_flag, a.status));
                 if (!ok) break;
                 if (split ? (j & 1) == t : j < mine) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->s_full[t]), own_no & 1, abort_flag, a.status));
+                    ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&sm->s_full[t]), own_no & 1, abort_flag, a.status));
                     if (!ok) break;
                     tc_fence_after();
                     if (any_live) {
@@ -510,75 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                 x[2 * i + 1] = mul2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k.y);
                             }
                         };
-                        // pass 1: the row's largest score
-                        float top = -INFINITY;
-                        if (!cut) {
-                            uint32_t buf[2][16];  // 16 columns of S while the next 16 are on their way
-                            tmem_ld16(s_col, buf[0]);
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                tmem_wait_ld();
-                                if (c < 7) tmem_ld16(s_col + 16 * (c + 1), buf[(c + 1) & 1]);
-                                uint64_t x[8];
-                                scores(buf[c & 1], c, x);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(unpack2(x[i]).x, unpack2(x[i]).y));
-                            }
-                        } else {
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
-                                uint32_t s[16];
-                                tmem_ld16(s_col + 16 * c, s);
-                                tmem_wait_ld();
-                                uint64_t x[8];
-                                scores(s, c, x);
-                                const uint32_t bits = seen(c);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    if ((bits >> (2 * i)) & 1) top = fmaxf(top, unpack2(x[i]).x);
-                                    if ((bits >> (2 * i)) & 2) top = fmaxf(top, unpack2(x[i]).y);
-                                }
-                                __syncwarp();
-                            }
-                        }
-                        top *= fr;
-                        // a new reference maximum or value exponent: rescale O
-                        const int ve = sm->vexp[sc];
-                        const bool grow = top > m + 8.f;
-                        if (__any_sync(0xffffffffu, grow) || ve != vcur) {
-                            const float mn = fmaxf(m, top);
-                            float f = ex2(m - mn);
-                            m = mn;
-                            l *= f;
-                            if (ve != vcur) f *= pow2i(max(-126, vcur - ve));
-                            vcur = ve;
-                            if (own > 0) {
-                                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->pv_done[t]), (own_no - 1) & 1,
-                                                                       abort_flag, a.status));
-                                if (!ok) break;
-                                tc_fence_after();
-#pragma unroll
-                                for (int c = 0; c < D / 32; ++c) {
-                                    uint32_t o[32];
-                                    tmem_ld32(o_col + 32 * c, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                    tmem_st32(o_col + 32 * c, o);
-                                }
-                                tmem_wait_st();
-                            }
-                        }
-                        // pass 2: weights
-                        const uint64_t fr2 = pack2(fr, fr), m2 = pack2(-m, -m);
-                        uint64_t l2 = 0;
-                        // eight pairs of scores -> weights; adds the unscaled ones to l2
-                        auto weights = [&](const uint64_t (&x)[8], int c, uint32_t (&p)[8]) {
+                        const uint64_t fr2 = pack2(fr, fr);
+                        // Eight pairs of scores over m -> weights; the unscaled ones' sum to l2.
+                        auto weights = [&](const uint64_t (&y)[8], int c, uint64_t &l2, uint32_t (&p)[8]) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const ulonglong2 v = vs2[4 * c + i];
-                                const float2 x0 = unpack2(fma2(x[2 * i], fr2, m2)), x1 = unpack2(fma2(x[2 * i + 1], fr2, m2));
-                                const uint64_t p0 = pack2(ex2(x0.x), ex2(x0.y)), p1 = pack2(ex2(x1.x), ex2(x1.y));
+                                const float2 y0 = unpack2(y[2 * i]), y1 = unpack2(y[2 * i + 1]);
+                                const uint64_t p0 = pack2(ex2(y0.x), ex2(y0.y)), p1 = pack2(ex2(y1.x), ex2(y1.y));
                                 l2 = add2(l2, p0);
                                 l2 = add2(l2, p1);
                                 const float2 w0 = unpack2(mul2(p0, v.x)), w1 = unpack2(mul2(p1, v.y));
@@ -587,37 +577,133 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                 p[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
                             }
                         };
-                        if (!cut) {
-                            uint32_t buf[2][16];
-                            tmem_ld16(s_col, buf[0]);
+                        // O, and P's first `cols` columns, times f.
+                        auto rescale = [&](float f, int cols) {
+                            if (own > 0) {
+                                if (!__all_sync(0xffffffffu, bar_wait(smem_u32(&sm->pv_done[t]), (own_no - 1) & 1,
+                                                                      abort_flag, a.status)))
+                                    return false;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D / 16; ++c) {
+                                    uint32_t o[16];
+                                    tmem_ld16(o_col + 16 * c, o);
+                                    tmem_wait_ld16(o);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tmem_st16(o_col + 16 * c, o);
+                                }
+                            }
+                            tmem_wait_st();
+                            const __half2 f2 = __float2half2_rn(f);  // a power of two where cols > 0
+#pragma unroll 1
+                            for (int c = 0; c < cols; c += 8) {
+                                uint32_t p[8];
+                                tmem_ld8(s_col + c, p);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&p[i]), f2);
+                                    p[i] = *reinterpret_cast<const uint32_t *>(&x);
+                                }
+                                tmem_st8(s_col + c, p);
+                            }
+                            tmem_wait_st();
+                            return true;
+                        };
+                        const int ve = sm->vexp[sc];
+                        if (!cut && ve == vcur && m != kNone) {
+                            // One pass with the maximum as it is.  Where a score exceeds it by more
+                            // than 2^8 (seldom), it moves by a whole number, so that what is done
+                            // already (sums, weights, O) is rescaled exactly.
+                            // (a sum of 16 weights up to 2^8 has none above it)
+                            uint32_t s[16];
+                            tmem_ld16(s_col, s);
+                            float lsum = 0.f;
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
-                                tmem_wait_ld();
-                                if (c < 7) tmem_ld16(s_col + 16 * (c + 1), buf[(c + 1) & 1]);
-                                uint64_t x[8];
-                                scores(buf[c & 1], c, x);
+                                ulonglong2 k[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) k[i] = ks2[4 * c + i];
+                                const uint64_t m2 = pack2(-m, -m);
+                                uint64_t y[8], l2 = 0;
                                 uint32_t p[8];
-                                weights(x, c, p);
+                                tmem_wait_ld16(s);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    y[2 * i] = fma2(mul2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k[i].x), fr2, m2);
+                                    y[2 * i + 1] = fma2(mul2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k[i].y), fr2, m2);
+                                }
+                                if (c < 7) tmem_ld16(s_col + 16 * (c + 1), s);
+                                weights(y, c, l2, p);
+                                float sum = unpack2(l2).x + unpack2(l2).y;
+                                if (__any_sync(0xffffffffu, sum > 256.f)) {
+                                    float top = 0.f;
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(unpack2(y[i]).x, unpack2(y[i]).y));
+                                    const float up = sum > 256.f ? ceilf(top) : 0.f, f = ex2(-up);
+                                    m += up;
+                                    l *= f;
+                                    lsum *= f;
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) y[i] = add2(y[i], pack2(-up, -up));
+                                    ok = rescale(f, 8 * c);
+                                    if (!ok) break;
+                                    l2 = 0;
+                                    weights(y, c, l2, p);
+                                    sum = unpack2(l2).x + unpack2(l2).y;
+                                }
+                                lsum += sum;
                                 tmem_st8(s_col + 8 * c, p);
                             }
+                            if (!ok) break;
+                            l += lsum;
                         } else {
+                            // pass 1: the row's largest score, in units of the row's power of two
+                            float top = -INFINITY;
 #pragma unroll 1
                             for (int c = 0; c < 8; ++c) {
                                 uint32_t s[16];
                                 tmem_ld16(s_col + 16 * c, s);
-                                tmem_wait_ld();
-                                uint64_t x[8];
-                                scores(s, c, x);
-                                const uint32_t bits = seen(c);
+                                tmem_wait_ld16(s);
+                                const uint32_t bits = cut ? seen(c) : 0xFFFFu;
                                 __syncwarp();
 #pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if ((bits >> i) & 1) top = fmaxf(top, __uint_as_float(s[i]) * sm->ks[sc][16 * c + i]);
+                            }
+                            top *= fr;
+                            // a new reference maximum or value exponent: rescale O
+                            if (__any_sync(0xffffffffu, top > m + 8.f) || ve != vcur) {
+                                const float mn = fmaxf(m, top);
+                                float f = ex2(m - mn);
+                                m = mn;
+                                l *= f;
+                                if (ve != vcur) f *= pow2i(max(-126, vcur - ve));
+                                vcur = ve;
+                                ok = rescale(f, 0);
+                                if (!ok) break;
+                            }
+                            // pass 2: weights
+                            const uint64_t m2 = pack2(-m, -m);
+                            uint64_t l2 = 0;
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t s[16], p[8];
+                                tmem_ld16(s_col + 16 * c, s);
+                                tmem_wait_ld16(s);
+                                const uint32_t bits = cut ? seen(c) : 0xFFFFu;
+                                __syncwarp();
+                                uint64_t y[8];
+#pragma unroll
                                 for (int i = 0; i < 8; ++i) {
-                                    const float2 y = unpack2(x[i]);
-                                    x[i] = pack2((bits >> (2 * i)) & 1 ? y.x : -INFINITY,
-                                                 (bits >> (2 * i)) & 2 ? y.y : -INFINITY);
+                                    const uint64_t x = pack2(__uint_as_float(s[2 * i]) * sm->ks[sc][16 * c + 2 * i],
+                                                             __uint_as_float(s[2 * i + 1]) * sm->ks[sc][16 * c + 2 * i + 1]);
+                                    const float2 z = unpack2(fma2(x, fr2, m2));
+                                    y[i] = pack2((bits >> (2 * i)) & 1 ? z.x : -INFINITY,
+                                                 (bits >> (2 * i)) & 2 ? z.y : -INFINITY);
                                 }
-                                uint32_t p[8];
-                                weights(x, c, p);
+                                weights(y, c, l2, p);
                                 // unseen: exactly zero, whatever the value row's scale is
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
@@ -626,9 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                 }
                                 tmem_st8(s_col + 8 * c, p);
                             }
+                            const float2 x = unpack2(l2);
+                            l += x.x + x.y;
                         }
-                        const float2 lp = unpack2(l2);
-                        l += lp.x + lp.y;
                         tmem_wait_st();
                     }
                     tc_fence_before();
@@ -642,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             if (!ok) break;
             // ---- the result ----
             if (own > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->pv_done[t]), (own_no - 1) & 1, abort_flag, a.status));
+                ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&sm->pv_done[t]), (own_no - 1) & 1, abort_flag, a.status));
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -734,25 +820,19 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
     } else if (warp < 8 + kWidenWarps) {
         // =============================== widening ===============================
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegWiden) : "memory");
-        const int tid = threadIdx.x - 256;
-        // A thread copies (cp.async) its own pieces of the codes into its own slots,
-        // kRawTiles tiles ahead, and page numbers are read one step before that.
-        constexpr int kN = L::kPieces;
-        constexpr int kRowPieces = kRow / 16;
-        const int piece = tid % kRowPieces, row0 = tid / kRowPieces;
-        constexpr int kRowStep = 32 * kWidenWarps / kRowPieces;  // rows between a thread's pieces
-        int pj = 0, id[kN], kv0 = 0, hi = 0, lo = 0, h = 0;
-        bool fetched = more;  // a step's page numbers are at hand
-        auto fetch_pages = [&]() {
-            kv0 = w.lo + (w.u0 + pj) * kStep;
+        // A warp serves 16 rows of every tile: one page, and one run of bytes in it.
+        // It copies them (cp.async) kRawTiles tiles ahead, and reads page numbers one
+        // step before that.
+        const int wr = (warp - 8) * 16;  // its first row
+        uint8_t *ring = base + L::kRaw + (warp - 8) * L::kRawWarp;
+        int pj = 0, id = -1, kv0 = 0, hi = 0, lo = 0, h = 0;
+        bool fetched = more;  // a step's page number is at hand
+        auto fetch_page = [&]() {
+            kv0 = w.lo + (w.u0 + pj) * kStep + wr;
             lo = w.s.lo, hi = w.hi, h = w.h;
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const int tile = (kv0 + row0 + i * kRowStep) >> 4;
-                int rest;
-                const int pg = page_of_tile(a, tile, &rest);
-                id[i] = pg < a.b.width && tile * 16 < hi ? __ldg(a.b.table + w.b * a.b.stride + pg) : -1;
-            }
+            int rest;
+            const int pg = page_of_tile(a, kv0 >> 4, &rest);
+            id = pg < a.b.width && kv0 < hi ? __ldg(a.b.table + w.b * a.b.stride + pg) : -1;
             if (++pj == w.u1 - w.u0) {
                 pj = 0;
                 more = warp_next(a, &w);
@@ -763,77 +843,78 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         auto issue = [&]() {  // the next tile: K of a step, then its V
             if (fetched) {
                 const bool is_v = issued & 1;
-                const uint32_t dst = smem_u32(base + L::kRaw + put * L::kRawTile) + tid * 16;
-                const uint8_t *codes = (is_v ? a.c.v : a.c.k) + piece * 16;
+                const uint32_t dst = smem_u32(ring + put * L::kRawTile);
+                const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.c.pages);
+                int rest;
+                page_of_tile(a, kv0 >> 4, &rest);
+                const int64_t rr = live ? (int64_t(id) * a.c.heads + h) * a.c.page + rest * 16 : 0;
+                const uint8_t *src = (is_v ? a.c.v : a.c.k) + rr * kRow + lane * 16;
+                const int v0 = live ? lo - kv0 : 16, v1 = hi - kv0;  // rows in use
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    const int at = kv0 + row0 + i * kRowStep;
-                    int rest;
-                    page_of_tile(a, at >> 4, &rest);
-                    const bool live = static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(a.c.pages) && at >= lo && at < hi;
-                    const int64_t rr = live ? (int64_t(id[i]) * a.c.heads + h) * a.c.page + rest * 16 + (at & 15) : 0;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512 * kWidenWarps),
-                                 "l"(codes + rr * kRow), "r"(live ? 16 : 0) : "memory");
-                    if (FMT == W4KV_INT4)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                                         dst - tid * 12 + (kN * 16 + i * 4) * 32 * kWidenWarps),
-                                     "l"((is_v ? a.c.vs : a.c.ks) + rr), "r"(live ? 4 : 0) : "memory");
+                for (int i = 0; i < (kRow + 31) / 32; ++i) {  // 512 bytes each
+                    const int row = (lane * 16 + i * 512) / kRow;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + lane * 16 + i * 512),
+                                 "l"(src + i * 512), "r"(row >= v0 && row < v1 ? 16 : 0) : "memory");
                 }
+                if (FMT == W4KV_INT4 && lane < 16)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 16 * kRow + lane * 4),
+                                 "l"((is_v ? a.c.vs : a.c.ks) + rr + lane), "r"(lane >= v0 && lane < v1 ? 4 : 0) : "memory");
                 ++issued;
                 if (is_v) {
                     fetched = more;
-                    if (fetched) fetch_pages();
+                    if (fetched) fetch_page();
                 }
             }
             put = put + 1 == L::kRawTiles ? 0 : put + 1;
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto store = [&](uint8_t *tile, const uint4 (&raw)[kN], const uint32_t (&z)[kN]) {
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                const int row = row0 + i * kRowStep;
-                if (FMT == W4KV_INT4) {
-                    const uint32_t zb = 0x64006400u | (z[i] & 15u) * 0x10001u;
-                    uint8_t *blk = tile + (piece >> 1) * L::kBlock;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {  // the lanes of a phase take different banks
-                        const int j = q ^ ((piece >> 1) * 2);
-                        const uint32_t xx = piece >> 1 ? x[q ^ 2] : x[q];
-                        *reinterpret_cast<uint4 *>(blk + swz(row, (piece & 1) * 4 + j)) = widen8_int4(xx, zb);
-                    }
-                } else {
-                    uint8_t *blk = tile + (piece >> 2) * L::kBlock;
-                    const uint2 h0 = widen4<FMT>(x[0]), h1 = widen4<FMT>(x[1]), h2 = widen4<FMT>(x[2]),
-                                h3 = widen4<FMT>(x[3]);
-                    const uint4 c0 = make_uint4(h0.x, h0.y, h1.x, h1.y), c1 = make_uint4(h2.x, h2.y, h3.x, h3.y);
-                    const int c = (piece & 3) * 2, flip = (piece >> 2) & 1;
-                    *reinterpret_cast<uint4 *>(blk + swz(row, c + flip)) = flip ? c1 : c0;
-                    *reinterpret_cast<uint4 *>(blk + swz(row, c + 1 - flip)) = flip ? c0 : c1;
-                }
-            }
-        };
-        if (fetched) fetch_pages();
+        if (fetched) fetch_page();
         for (int i = 0; i < L::kRawTiles; ++i) issue();
+        // Eight codes make one 16-byte chunk; the lanes of a phase write the chunks of
+        // one row, which lie in different banks.
+        constexpr int kRowChunks = D / 8, kRowsAtOnce = 32 / kRowChunks, kN = 16 / kRowsAtOnce;
+        const int chunk = lane % kRowChunks, r0 = lane / kRowChunks;
+        const int st_off = (chunk >> 3) * L::kBlock;
         int get = 0;
+        uint32_t buf = 0, phase = 1;
         for (uint32_t n = 0; n < issued; ++n) {
-            const uint32_t buf = n % kBuffers;
             asm volatile("cp.async.wait_group %0;" ::"n"(L::kRawTiles - 1) : "memory");
-            const uint8_t *src = base + L::kRaw + get * L::kRawTile;
-            uint4 raw[kN];
+            __syncwarp();
+            const uint8_t *src = ring + get * L::kRawTile;
+            uint2 raw[kN];
             uint32_t z[kN];
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
-                raw[i] = *reinterpret_cast<const uint4 *>(src + tid * 16 + i * 512 * kWidenWarps);
-                z[i] = FMT == W4KV_INT4 ? *reinterpret_cast<const uint32_t *>(src + tid * 4 + (kN * 16 + i * 4) * 32 * kWidenWarps) : 0u;
+                const int row = r0 + i * kRowsAtOnce;
+                if (FMT == W4KV_INT4) {
+                    raw[i].x = *reinterpret_cast<const uint32_t *>(src + row * kRow + chunk * 4);
+                    z[i] = *reinterpret_cast<const uint32_t *>(src + 16 * kRow + row * 4);
+                } else {
+                    raw[i] = *reinterpret_cast<const uint2 *>(src + row * kRow + chunk * 8);
+                }
             }
             get = get + 1 == L::kRawTiles ? 0 : get + 1;
+            __syncwarp();
             issue();
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->empty[buf]), ((n / kBuffers) & 1) ^ 1, abort_flag, a.status)))
-                break;
-            store(base + L::kKV + buf * L::kTile, raw, z);
+            if (!__all_sync(0xffffffffu, bar_wait(smem_u32(&sm->empty[buf]), phase, abort_flag, a.status))) break;
+            uint8_t *tile = base + L::kKV + buf * L::kTile + st_off + wr * 128;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                uint4 x;
+                if (FMT == W4KV_INT4) {
+                    x = widen8_int4(raw[i].x, 0x64006400u | (z[i] & 15u) * 0x10001u);
+                } else {
+                    const uint2 h0 = widen4<FMT>(raw[i].x), h1 = widen4<FMT>(raw[i].y);
+                    x = make_uint4(h0.x, h0.y, h1.x, h1.y);
+                }
+                *reinterpret_cast<uint4 *>(tile + swz(r0 + i * kRowsAtOnce, chunk & 7)) = x;
+            }
             fence_proxy_async();
             mbar_arrive(smem_u32(&sm->full[buf]));
+            if (++buf == kBuffers) {
+                buf = 0;
+                phase ^= 1;
+            }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
@@ -852,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         uint32_t step0 = 0, seg_no = 0, n_p = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(bar), parity, abort_flag, a.status));
+            ok = __all_sync(0xffffffffu, ok && bar_wait(smem_u32(bar), parity, abort_flag, a.status));
             return ok;
         };
         for (; more && ok; more = warp_next(a, &w), ++seg_no) {
@@ -881,9 +962,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                         mma_commit(smem_u32(&sm->empty[kb]));
                     }
                     __syncwarp();
-                    if (!wait(&sm->p_full[t], n_p++ & 1)) break;
                 }
                 if (!wait(&sm->full[vb], (vn / kBuffers) & 1)) break;
+                if (own && !wait(&sm->p_full[t], n_p++ & 1)) break;
                 if (!own) {
                     if (lane == 0) mbar_arrive(smem_u32(&sm->empty[vb]));
                 } else {
@@ -969,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             // of the item's part: the streams start anew with each
             vexp = max(info >> 31 ? 7 : vexp, static_cast<int>(__reduce_max_sync(0xffffffffu, ve)));
             const float vmul = pow2i(133 - vexp);
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm->sc_empty[sc]),
+            if (!__all_sync(0xffffffffu, bar_wait(smem_u32(&sm->sc_empty[sc]),
                                                    ((step_no / kScaleStages) & 1) ^ 1, abort_flag, a.status)))
                 break;
 #pragma unroll
