@@ -175,7 +175,7 @@ struct alignas(16) Control {
     Walk walk[8 + kWidenWarps + 4];  // of each warp: read by all its lanes, moved by lane 0
     RangeSmem range;
     uint32_t tmem;
-    int abort_flag;
+    int abort_flag, mma_lock;
 };
 
 template <int FMT, int D>
@@ -225,6 +225,21 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     }
     return true;
 }
+
+// A lock between the threads that issue MMAs; a wait that runs out goes on without it.
+__device__ __forceinline__ void lock(int *word, volatile int *abort_flag, unsigned *status) {
+    if (atomicCAS_block(word, 0, 1) == 0) return;
+    const unsigned long long t0 = globaltimer();
+    while (atomicCAS_block(word, 0, 1) != 0) {
+        if (*abort_flag) return;
+        if (globaltimer() - t0 > kWaitNs) {
+            *abort_flag = 1;
+            atomicOr(status, 1u);
+            return;
+        }
+    }
+}
+__device__ __forceinline__ void unlock(int *word) { atomicExch_block(word, 0); }
 
 // kind::f16, D f32, A and B fp16, M = 128; kTransB: B is MN-major.
 template <int N, bool kTransB>
@@ -430,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         }
         mbar_init(smem_u32(&sm->joined), 2 * kM);
         sm->abort_flag = 0;
+        sm->mma_lock = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const Range range = block_range<kThreads>(a.b.n, &sm->range, [&](int b) -> int64_t {
@@ -940,45 +956,81 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             const bool split = w.R <= kM;
             const int ns = w.u1 - w.u0, mine = stream_steps(a, w, t);
             if (!wait(&sm->q_full[t], seg_no & 1)) break;
+            auto filled = [&](uint32_t n) { return wait(&sm->full[n % kBuffers], (n / kBuffers) & 1); };
+            auto let_go = [&](uint32_t n) {
+                if (lane == 0) mbar_arrive(smem_u32(&sm->empty[n % kBuffers]));
+            };
+            auto score = [&](uint32_t n) {  // S from the keys in tile n (one thread)
+                const uint32_t k = k0 + (n % kBuffers) * (L::kTile >> 4);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = ((x / 4) * L::kBlock + (x % 4) * 32) >> 4;
+                    mma_ss(d_s, q + off, k + off, id_s, x > 0);
+                }
+                mma_commit(smem_u32(&sm->s_full[t]));
+                mma_commit(smem_u32(&sm->empty[n % kBuffers]));
+            };
+            auto output = [&](uint32_t n, bool first) {  // O from the values in tile n (one thread)
+                const uint32_t v = v0 + (n % kBuffers) * (L::kTile >> 4);
+#pragma unroll
+                for (int x = 0; x < kStep / 16; ++x)
+                    mma_ts(d_o, d_s + 8 * x, v + x * (2048 >> 4), id_o, !(first && x == 0));
+                mma_commit(smem_u32(&sm->pv_done[t]));
+                mma_commit(smem_u32(&sm->empty[n % kBuffers]));
+            };
             // Tiles are taken, or let go, in the order they are widened.
-            bool first = true;
-            for (int j = 0; j < ns && ok; ++j) {
-                const bool own = split ? (j & 1) == t : j < mine;
-                const uint32_t kn = 2 * (step0 + j), vn = kn + 1;
-                const uint32_t kb = kn % kBuffers, vb = vn % kBuffers;
-                if (!wait(&sm->full[kb], (kn / kBuffers) & 1)) break;
-                if (!own) {
-                    if (lane == 0) mbar_arrive(smem_u32(&sm->empty[kb]));
-                } else {
+            if (split) {
+                bool first = true;
+                for (int j = 0; j < ns && ok; ++j) {
+                    const bool own = (j & 1) == t;
+                    const uint32_t n = 2 * (step0 + j);
+                    if (!filled(n)) break;
+                    if (!own) {
+                        let_go(n);
+                    } else {
+                        tc_fence_after();
+                        if (elect_one()) score(n);
+                        __syncwarp();
+                    }
+                    if (!filled(n + 1)) break;
+                    if (!own) {
+                        let_go(n + 1);
+                    } else {
+                        if (!wait(&sm->p_full[t], n_p++ & 1)) break;
+                        tc_fence_after();
+                        if (elect_one()) output(n + 1, first);
+                        __syncwarp();
+                        first = false;
+                    }
+                }
+            } else {
+                // O(j) and S(j + 1) go to the tensor cores together: the streams' MMAs do
+                // not mix, so that the first one's softmax starts while the other's run.
+                if (mine > 0) {
+                    if (!filled(2 * step0)) break;
+                    tc_fence_after();
+                    if (elect_one()) score(2 * step0);
+                    __syncwarp();
+                }
+                for (int j = 0; j < mine && ok; ++j) {
+                    const uint32_t n = 2 * (step0 + j) + 1;
+                    const bool next = j + 1 < mine;
+                    if (!filled(n) || (next && !filled(n + 1))) break;
+                    if (!wait(&sm->p_full[t], n_p++ & 1)) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t k = k0 + kb * (L::kTile >> 4);
-#pragma unroll
-                        for (int x = 0; x < D / 16; ++x) {
-                            const uint32_t off = ((x / 4) * L::kBlock + (x % 4) * 32) >> 4;
-                            mma_ss(d_s, q + off, k + off, id_s, x > 0);
-                        }
-                        mma_commit(smem_u32(&sm->s_full[t]));
-                        mma_commit(smem_u32(&sm->empty[kb]));
+                        lock(&sm->mma_lock, abort_flag, a.status);
+                        output(n, j == 0);
+                        if (next) score(n + 1);
+                        unlock(&sm->mma_lock);
                     }
                     __syncwarp();
                 }
-                if (!wait(&sm->full[vb], (vn / kBuffers) & 1)) break;
-                if (own && !wait(&sm->p_full[t], n_p++ & 1)) break;
-                if (!own) {
-                    if (lane == 0) mbar_arrive(smem_u32(&sm->empty[vb]));
-                } else {
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t v = v0 + vb * (L::kTile >> 4);
-#pragma unroll
-                        for (int x = 0; x < kStep / 16; ++x)
-                            mma_ts(d_o, d_s + 8 * x, v + x * (2048 >> 4), id_o, !(first && x == 0));
-                        mma_commit(smem_u32(&sm->pv_done[t]));
-                        mma_commit(smem_u32(&sm->empty[vb]));
-                    }
-                    __syncwarp();
-                    first = false;
+                for (int j = mine; j < ns && ok; ++j) {  // steps that tile A does not see
+                    if (!filled(2 * (step0 + j))) break;
+                    let_go(2 * (step0 + j));
+                    if (!filled(2 * (step0 + j) + 1)) break;
+                    let_go(2 * (step0 + j) + 1);
                 }
             }
             step0 += ns;
