@@ -31,6 +31,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "w4_tc.cuh"
 #include "w4kv_attn.cuh"
 
@@ -628,15 +630,37 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                             return true;
                         };
                         const int ve = sm->vexp[sc];
-                        if (!cut && ve == vcur && m != kNone) {
-                            // One pass with the maximum as it is.  Where a score exceeds it by more
-                            // than 2^8 (seldom), it moves by a whole number, so that what is done
-                            // already (sums, weights, O) is rescaled exactly.
-                            // (a sum of 16 weights up to 2^8 has none above it)
+                        if (ve != vcur) {  // the value scales' reference moved
+                            ok = rescale(pow2i(max(-126, vcur - ve)), 0);
+                            if (!ok) break;
+                            vcur = ve;
+                        }
+                        if (__any_sync(0xffffffffu, m == kNone)) {
+                            // Rows that have seen nothing yet start from their largest score.
+                            float top = -INFINITY;
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t s[16];
+                                tmem_ld16(s_col + 16 * c, s);
+                                tmem_wait_ld16(s);
+                                const uint32_t bits = cut ? seen(c) : 0xFFFFu;
+                                __syncwarp();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if ((bits >> i) & 1) top = fmaxf(top, __uint_as_float(s[i]) * sm->ks[sc][16 * c + i]);
+                            }
+                            if (m == kNone) m = fmaxf(m, top * fr);
+                        }
+                        // One pass with the maximum as it is.  Where a score exceeds it by more
+                        // than 2^8 (seldom), it moves by a whole number, so that what is done
+                        // already (sums, weights, O) is rescaled exactly.  (A sum of weights up
+                        // to 2^8 has none above it.)
+                        auto weigh = [&](auto cut_tag) {
+                            constexpr bool kCut = decltype(cut_tag)::value;
                             uint32_t s[16];
                             tmem_ld16(s_col, s);
                             float lsum = 0.f;
-#pragma unroll
+#pragma unroll(kCut ? 1 : 8)
                             for (int c = 0; c < 8; ++c) {
                                 ulonglong2 k[4];
 #pragma unroll
@@ -651,6 +675,15 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                     y[2 * i + 1] = fma2(mul2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k[i].y), fr2, m2);
                                 }
                                 if (c < 7) tmem_ld16(s_col + 16 * (c + 1), s);
+                                const uint32_t bits = kCut ? seen(c) : 0xFFFFu;
+                                if (kCut) {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const float2 z = unpack2(y[i]);
+                                        y[i] = pack2((bits >> (2 * i)) & 1 ? z.x : -INFINITY,
+                                                     (bits >> (2 * i)) & 2 ? z.y : -INFINITY);
+                                    }
+                                }
                                 weights(y, c, l2, p);
                                 float sum = unpack2(l2).x + unpack2(l2).y;
                                 if (__any_sync(0xffffffffu, sum > 256.f)) {
@@ -664,73 +697,27 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) y[i] = add2(y[i], pack2(-up, -up));
                                     ok = rescale(f, 8 * c);
-                                    if (!ok) break;
+                                    if (!ok) return;
                                     l2 = 0;
                                     weights(y, c, l2, p);
                                     sum = unpack2(l2).x + unpack2(l2).y;
                                 }
+                                if (kCut) {  // unseen: exactly zero, whatever the value row's scale is
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const uint32_t two = (bits >> (2 * i)) & 3u;
+                                        p[i] &= (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+                                    }
+                                }
                                 lsum += sum;
+                                if (kCut) __syncwarp();
                                 tmem_st8(s_col + 8 * c, p);
                             }
-                            if (!ok) break;
                             l += lsum;
-                        } else {
-                            // pass 1: the row's largest score, in units of the row's power of two
-                            float top = -INFINITY;
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
-                                uint32_t s[16];
-                                tmem_ld16(s_col + 16 * c, s);
-                                tmem_wait_ld16(s);
-                                const uint32_t bits = cut ? seen(c) : 0xFFFFu;
-                                __syncwarp();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if ((bits >> i) & 1) top = fmaxf(top, __uint_as_float(s[i]) * sm->ks[sc][16 * c + i]);
-                            }
-                            top *= fr;
-                            // a new reference maximum or value exponent: rescale O
-                            if (__any_sync(0xffffffffu, top > m + 8.f) || ve != vcur) {
-                                const float mn = fmaxf(m, top);
-                                float f = ex2(m - mn);
-                                m = mn;
-                                l *= f;
-                                if (ve != vcur) f *= pow2i(max(-126, vcur - ve));
-                                vcur = ve;
-                                ok = rescale(f, 0);
-                                if (!ok) break;
-                            }
-                            // pass 2: weights
-                            const uint64_t m2 = pack2(-m, -m);
-                            uint64_t l2 = 0;
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
-                                uint32_t s[16], p[8];
-                                tmem_ld16(s_col + 16 * c, s);
-                                tmem_wait_ld16(s);
-                                const uint32_t bits = cut ? seen(c) : 0xFFFFu;
-                                __syncwarp();
-                                uint64_t y[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const uint64_t x = pack2(__uint_as_float(s[2 * i]) * sm->ks[sc][16 * c + 2 * i],
-                                                             __uint_as_float(s[2 * i + 1]) * sm->ks[sc][16 * c + 2 * i + 1]);
-                                    const float2 z = unpack2(fma2(x, fr2, m2));
-                                    y[i] = pack2((bits >> (2 * i)) & 1 ? z.x : -INFINITY,
-                                                 (bits >> (2 * i)) & 2 ? z.y : -INFINITY);
-                                }
-                                weights(y, c, l2, p);
-                                // unseen: exactly zero, whatever the value row's scale is
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const uint32_t two = (bits >> (2 * i)) & 3u;
-                                    p[i] &= (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
-                                }
-                                tmem_st8(s_col + 8 * c, p);
-                            }
-                            const float2 x = unpack2(l2);
-                            l += x.x + x.y;
-                        }
+                        };
+                        if (cut) weigh(std::true_type());
+                        else weigh(std::false_type());
+                        if (!ok) break;
                         tmem_wait_st();
                     }
                     tc_fence_before();
