@@ -18,7 +18,7 @@ namespace {
 // Item that starts in block blockIdx.x and ends in a later one: the weighted
 // mean of its blocks' normalized outputs.
 template <int XT>
-__global__ void __launch_bounds__(256) combine_kernel(const Attn a, int tile, int dim) {
+__global__ void __launch_bounds__(256) combine_kernel(const Attn a, int tile, int dim, bool side) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 d = a.desc[blockIdx.x];
     if (d.z == 0) return;
@@ -29,7 +29,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const Attn a, int tile, in
     const float *first = a.slots + (2 * int64_t(blockIdx.x) + 1) * slot;
     const float *rest = a.slots + 2 * int64_t(blockIdx.x) * slot;  // + 2 i slots for block + i
     for (int i = blockIdx.y * 256 + threadIdx.x; i < R * dim / 4; i += 256 * gridDim.y) {
-        const int r = i / (dim / 4), e = (i - r * (dim / 4)) * 4;
+        // `side`: four dims of a row after another, rows side by side
+        const int r = side ? i % R : i / (dim / 4), e = (side ? i / R : i - r * (dim / 4)) * 4;
+        const int64_t at = 2 * tile + (side ? int64_t(e) * tile + 4 * r : int64_t(r) * dim + e);
         float M = first[r];
         for (int q = 1; q < d.z; ++q) M = fmaxf(M, rest[2 * q * slot + r]);
         float L = 0.f;
@@ -38,7 +40,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Attn a, int tile, in
         for (int q = 0; q < d.z; ++q) {
             const float *p = q ? rest + 2 * q * slot : first;
             const float w = p[tile + r] * ex2(p[r] - M);
-            const float4 v = *reinterpret_cast<const float4 *>(p + 2 * tile + r * dim + e);
+            const float4 v = *reinterpret_cast<const float4 *>(p + at);
             L += w;
             o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
             o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
@@ -68,8 +70,9 @@ int launch_combine(const Attn &a, int grid, int tile, int dim, int xt, cudaStrea
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cuda_status(xt == W4_F16 ? cudaLaunchKernelEx(&cfg, combine_kernel<W4_F16>, a, tile, dim)
-                                    : cudaLaunchKernelEx(&cfg, combine_kernel<W4_BF16>, a, tile, dim));
+    const bool side = tile == kTiledRows;
+    return cuda_status(xt == W4_F16 ? cudaLaunchKernelEx(&cfg, combine_kernel<W4_F16>, a, tile, dim, side)
+                                    : cudaLaunchKernelEx(&cfg, combine_kernel<W4_BF16>, a, tile, dim, side));
 }
 
 namespace {
@@ -153,6 +156,8 @@ int w4kv_attention(const w4kv_cache *cache, const w4kv_batch *batch, const void 
     DeviceInfo d;
     if ((st = device_info(&d)) != W4_OK) return st;
     if (max_rows > rows) max_rows = rows;
+    if (max_rows * (heads / a.c.heads) > 0x7FFFFFFF - kTiledRows)
+        return set_error(W4_ERR_INVALID_ARG, fn, "max_rows * heads / kv_heads too large");
     const Plan p = make_plan(d, D, a.b.n, max_rows, heads / a.c.heads);
     if (p.total > 0 && (!workspace || workspace_bytes < p.total ||
                         (reinterpret_cast<uintptr_t>(workspace) & 255u)))

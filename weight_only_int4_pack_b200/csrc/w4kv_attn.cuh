@@ -175,7 +175,8 @@ __device__ __forceinline__ int block_of_unit(int64_t u, const Range &r) {
 constexpr float kNone = -1e30f;
 
 // A partial result: maxima and sums (base 2) and the normalized output of
-// `rows` rows: [rows] + [rows] + [rows][dim] floats.
+// `rows` rows: [rows] + [rows] + [rows][dim] floats (the tiled kernel's output:
+// [dim / 4][rows][4]).
 __host__ __device__ constexpr int64_t slot_floats(int rows, int dim) {
     return int64_t(rows) * (dim + 2);
 }

@@ -71,10 +71,10 @@ struct Walk {
 };
 
 __device__ __forceinline__ void tile_bounds(const Attn &a, const Seq &s, int tile, int *lo, int *hi) {
-    const int64_t r0 = int64_t(tile) * kTileRows;
-    const int64_t r1 = min(int64_t(s.n) * a.group, r0 + kTileRows) - 1;
-    *hi = a.causal ? min(s.hi, max(0, s.first + static_cast<int>(r1 / a.group) + 1)) : s.hi;
-    *lo = a.window > 0 ? max(0, s.first + static_cast<int>(r0 / a.group) + 1 - a.window) : 0;
+    const int r0 = tile * kTileRows;  // rows * group of a call is below 2^31
+    const int r1 = min(s.n * a.group, r0 + kTileRows) - 1;
+    *hi = a.causal ? min(s.hi, max(0, s.first + r1 / a.group + 1)) : s.hi;
+    *lo = a.window > 0 ? max(0, s.first + r0 / a.group + 1 - a.window) : 0;
     *lo = min(*lo, *hi) & ~15;
 }
 
@@ -85,14 +85,14 @@ __device__ __forceinline__ int tile_units(const Attn &a, const Seq &s, int tile)
 }
 
 __device__ __forceinline__ int seq_tiles(const Attn &a, const Seq &s) {
-    return static_cast<int>((int64_t(s.n) * a.group + kTileRows - 1) / kTileRows);
+    return (s.n * a.group - 1) / kTileRows + 1;
 }
 
 __device__ __forceinline__ void set_item(const Attn &a, Walk &w) {
     tile_bounds(a, w.s, w.tile, &w.lo, &w.hi);
     w.nu = max(1, (w.hi - w.lo + kStep - 1) / kStep);
     w.r0 = w.tile * kTileRows;
-    w.R = static_cast<int>(min(static_cast<int64_t>(kTileRows), int64_t(w.s.n) * a.group - w.r0));
+    w.R = min(kTileRows, w.s.n * a.group - w.r0);
 }
 
 // Opens the segment (the part of one item in the block's range) at w.x.
@@ -501,37 +501,51 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             const int rr = w.r0 + r;
             const int token = rr / a.group, head = w.h * a.group + rr - token * a.group;
             // ---- the query row: scaled by a power of two, fp16, swizzled ----
-            float fr;
+            // D / 8 lanes read a row together; lane i keeps the factor of row i of the warp.
+            float fr = 1.f;
             {
-                const uint16_t *qp = a.q + int64_t(w.s.row0 + token) * a.q_row + head * a.q_head;
-                uint32_t top = 0;
-                if (live) {
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+                const int part = lane % kLanes, sub = lane / kLanes;
+                uint8_t *qs = base + L::kQ + t * L::kTile + (part >> 3) * L::kBlock;
+#pragma unroll 1
+                for (int i = 0; i < 32; i += 8 * kAtOnce) {
+                    uint4 v[8];
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qp) + i);
-                        const uint32_t x = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                                    __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-                        top = max(top, max(x & 0xFFFFu, x >> 16));
+                    for (int q = 0; q < 8; ++q) {  // all loads first
+                        const int lr = i + q * kAtOnce + sub, x = (row & ~31) + lr + (split ? 0 : t * kM);
+                        const int y = w.r0 + x, tok = y / a.group;
+                        v[q] = x < w.R ? __ldg(reinterpret_cast<const uint4 *>(
+                                                   a.q + int64_t(w.s.row0 + tok) * a.q_row +
+                                                   (w.h * a.group + y - tok * a.group) * a.q_head) + part)
+                                       : make_uint4(0, 0, 0, 0);
                     }
-                }
-                int sh = 0;  // the row times 2^sh has its largest element in [2^4, 2^5)
-                const uint32_t t32 = __float_as_uint(widen1<XT>(static_cast<uint16_t>(top)));
-                if (t32 != 0 && t32 < 0x7F800000u) sh = min(120, 131 - static_cast<int>(t32 >> 23));
-                const float up = pow2i(sh);
-                fr = pow2i(-sh);
-                uint8_t *qs = base + L::kQ + t * L::kTile;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    float e[8];
-                    widen8<XT>(live ? __ldg(reinterpret_cast<const uint4 *>(qp) + i) : make_uint4(0, 0, 0, 0), e);
-                    uint32_t h[4];
+                    for (int q = 0; q < 8; ++q) {
+                        const int lr = i + q * kAtOnce + sub;
+                        const uint32_t x = __vmaxu2(__vmaxu2(v[q].x & 0x7FFF7FFFu, v[q].y & 0x7FFF7FFFu),
+                                                    __vmaxu2(v[q].z & 0x7FFF7FFFu, v[q].w & 0x7FFF7FFFu));
+                        uint32_t top = max(x & 0xFFFFu, x >> 16);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const __half2 p = __floats2half2_rn(e[2 * j] * up, e[2 * j + 1] * up);
-                        h[j] = *reinterpret_cast<const uint32_t *>(&p);
+                        for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        int sh = 0;  // the row times 2^sh has its largest element in [2^4, 2^5)
+                        const uint32_t t32 = __float_as_uint(widen1<XT>(static_cast<uint16_t>(top)));
+                        if (t32 != 0 && t32 < 0x7F800000u) sh = min(120, 131 - static_cast<int>(t32 >> 23));
+                        const float up = pow2i(sh);
+                        float e[8];
+                        widen8<XT>(v[q], e);
+                        uint32_t h[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const __half2 p = __floats2half2_rn(e[2 * j] * up, e[2 * j + 1] * up);
+                            h[j] = *reinterpret_cast<const uint32_t *>(&p);
+                        }
+                        *reinterpret_cast<uint4 *>(qs + swz((row & ~31) + lr, part & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+                        for (int o = 0; o < kAtOnce; ++o) {
+                            const int s2 = __shfl_sync(0xffffffffu, sh, o * kLanes);
+                            if (lane == i + q * kAtOnce + o) fr = pow2i(-s2);
+                        }
                     }
-                    *reinterpret_cast<uint4 *>(qs + (i / 8) * L::kBlock + swz(row, i & 7)) =
-                        make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 fence_proxy_async();
                 mbar_arrive(smem_u32(&sm->q_full[t]));
@@ -643,11 +657,26 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                 uint32_t s[16];
                                 tmem_ld16(s_col + 16 * c, s);
                                 tmem_wait_ld16(s);
-                                const uint32_t bits = cut ? seen(c) : 0xFFFFu;
-                                __syncwarp();
+                                float x[16];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if ((bits >> i) & 1) top = fmaxf(top, __uint_as_float(s[i]) * sm->ks[sc][16 * c + i]);
+                                for (int i = 0; i < 4; ++i) {
+                                    const float4 k = reinterpret_cast<const float4 *>(sm->ks[sc])[4 * c + i];
+                                    x[4 * i] = __uint_as_float(s[4 * i]) * k.x;
+                                    x[4 * i + 1] = __uint_as_float(s[4 * i + 1]) * k.y;
+                                    x[4 * i + 2] = __uint_as_float(s[4 * i + 2]) * k.z;
+                                    x[4 * i + 3] = __uint_as_float(s[4 * i + 3]) * k.w;
+                                }
+                                if (cut) {
+                                    const uint32_t bits = seen(c);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) x[i] = (bits >> i) & 1 ? x[i] : -INFINITY;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[i] = fmaxf(x[i], x[i + 8]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) x[i] = fmaxf(x[i], x[i + 4]);
+                                top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+                                __syncwarp();
                             }
                             if (m == kNone) m = fmaxf(m, top * fr);
                         }
@@ -780,10 +809,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                             reinterpret_cast<uint4 *>(op)[i] = make_uint4(h[0], h[1], h[2], h[3]);
                         }
                     } else if (live) {
-                        float4 *sp = reinterpret_cast<float4 *>(slot + 2 * kTileRows + int64_t(r) * D + 32 * c);
+                        // four dims of a row after another, rows side by side
+                        float4 *sp = reinterpret_cast<float4 *>(slot + 2 * kTileRows) + 8 * c * kTileRows + r;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            sp[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                            sp[i * kTileRows] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                     }
                     __syncwarp();
                 }
