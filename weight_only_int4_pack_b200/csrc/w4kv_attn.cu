@@ -88,14 +88,17 @@ struct Plan {
     size_t total = 0;
 };
 
+// (row, head) pairs per key/value head up to which the row kernel serves a sequence.
+constexpr int kRowsLimit = 64;
+
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 Plan make_plan(const DeviceInfo &d, int dim, int64_t batch, int64_t max_rows, int group) {
     Plan p;
     const int64_t pairs = max_rows * group;
     if (pairs <= 8) p.rows.tile = 8;
-    else if (pairs <= 16 || (batch > 1 && group <= 16)) p.rows.tile = 16;
-    if (pairs > 16) p.tiled.tile = kTiledRows;
+    else if (pairs <= kRowsLimit || (batch > 1 && group <= kRowsLimit)) p.rows.tile = 16;
+    if (pairs > kRowsLimit) p.tiled.tile = kTiledRows;
     p.rows.grid = rows_blocks_per_sm(p.rows.tile) * d.sm_count;
     p.tiled.grid = d.sm_count;
     for (Launch *l : {&p.rows, &p.tiled}) {
@@ -184,10 +187,10 @@ int w4kv_attention(const w4kv_cache *cache, const w4kv_batch *batch, const void 
     a.min_rows = 0;
     if (p.rows.tile) {
         partials(p.rows);
-        a.max_served = p.rows.tile;
+        a.max_served = p.rows.tile == 8 ? 8 : kRowsLimit;
         if ((st = launch_rows_attention(a, cache->fmt, D, xt, p.rows.tile, p.rows.grid, s)) != W4_OK) return st;
         if ((st = launch_combine(a, p.rows.grid, p.rows.tile, D, xt, s)) != W4_OK) return st;
-        a.min_rows = p.rows.tile;
+        a.min_rows = a.max_served;
     }
     if (p.tiled.tile) {
         partials(p.tiled);

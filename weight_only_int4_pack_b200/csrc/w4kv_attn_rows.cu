@@ -162,11 +162,12 @@ __device__ __forceinline__ int key_dim(int c, int s) {
 // Where a walk over the block's units stands: an item and its tiles.
 struct Walk {
     Seq s;
-    int b, h;         // sequence, key/value head
+    int b, h, tile;   // sequence, key/value head, tile of its (row, head) pairs
+    int lo, hi;       // cached positions that the tile's rows see
     int x, nu;        // walked of the item, in cost; its units
     int64_t rem;      // cost of the block's range not yet walked
     int u0, u1;       // units of the current segment (the item's part in the block's range)
-    int tile, end;    // its tiles: this warp's next one, the first behind it
+    int next, end;    // its 16-token tiles: this warp's next one, the first behind it
 };
 
 template <int FMT, int D, int XT, int NT>
@@ -184,12 +185,20 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
         smem + ((S::kRing + S::kJoin + S::kStats + 15) & ~15));
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    auto item_units = [](const Seq &s) {
-        return max(1, ((s.hi + 15) / 16 - s.lo / 16 + kUnit / 16 - 1) / (kUnit / 16));
+    auto tiles_of = [&](const Seq &s) { return (s.n * a.group - 1) / S::kTileRows + 1; };
+    auto tile_range = [&](const Seq &s, int tile, int *lo, int *hi) {
+        const int r0 = tile * S::kTileRows, r1 = min(s.n * a.group, r0 + S::kTileRows) - 1;
+        *hi = a.causal ? min(s.hi, max(0, s.first + r1 / a.group + 1)) : s.hi;
+        *lo = a.window > 0 ? min(*hi, max(0, s.first + r0 / a.group + 1 - a.window)) : 0;
+        return max(1, ((*hi + 15) / 16 - *lo / 16 + kUnit / 16 - 1) / (kUnit / 16));  // units
     };
     const Range range = block_range<kThreads>(a.b.n, rsm, [&](int b) -> int64_t {
         const Seq s = load_seq(a, b);
-        return s.n > 0 ? int64_t(kItemCost + item_units(s)) * a.c.heads : 0;
+        if (s.n == 0) return 0;
+        const int tiles = tiles_of(s);
+        int cost = 0, lo, hi;
+        for (int t = 0; t < tiles; ++t) cost += kItemCost + tile_range(s, t, &lo, &hi);
+        return int64_t(cost) * a.c.heads;
     });
     if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     if (range.start == range.end) return;
@@ -201,27 +210,40 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
         w.u1 = max(0, x1 - kItemCost);
         w.rem -= x1 - w.x;
         w.x = x1;
-        const int t0 = w.s.lo / 16;
-        w.tile = t0 + w.u0 * (kUnit / 16) + warp;
-        w.end = min((w.s.hi + 15) / 16, t0 + w.u1 * (kUnit / 16));
+        const int t0 = w.lo / 16;
+        w.next = t0 + w.u0 * (kUnit / 16) + warp;
+        w.end = min((w.hi + 15) / 16, t0 + w.u1 * (kUnit / 16));
     };
     auto next_item = [&](Walk &w) {  // only while w.rem > 0: a later item exists
         w.x = 0;
-        if (++w.h == a.c.heads) {
+        if (++w.tile == tiles_of(w.s)) {
+            w.tile = 0;
+            ++w.h;
+        }
+        if (w.h == a.c.heads) {
             w.h = 0;
             do {
                 if (w.b + 1 < a.b.n) ++w.b;
                 w.s = load_seq(a, w.b);
             } while (w.s.n == 0 && w.b + 1 < a.b.n);
-            w.nu = item_units(w.s);
         }
+        w.nu = tile_range(w.s, w.tile, &w.lo, &w.hi);
     };
     Walk w;
     w.b = range.b;
     w.s = load_seq(a, w.b);
-    w.nu = item_units(w.s);
-    w.h = static_cast<int>(range.off / (w.nu + kItemCost));
-    w.x = static_cast<int>(range.off % (w.nu + kItemCost));
+    {
+        const int tiles = tiles_of(w.s);
+        int per_head = 0;
+        for (int t = 0; t < tiles; ++t) per_head += kItemCost + tile_range(w.s, t, &w.lo, &w.hi);
+        w.h = static_cast<int>(range.off / per_head);
+        w.x = static_cast<int>(range.off % per_head);
+        for (w.tile = 0;; ++w.tile) {
+            w.nu = tile_range(w.s, w.tile, &w.lo, &w.hi);
+            if (w.x < w.nu + kItemCost || w.tile + 1 >= tiles) break;
+            w.x -= w.nu + kItemCost;
+        }
+    }
     w.rem = range.end - range.start;
     open(w);
     Walk p = w;  // the producer's walk, ahead of the consumer's
@@ -230,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
     int p_id = 0, p_rest = 0;
     bool p_live = true;  // a tile is left to issue
     auto fetch_page = [&]() {
-        while (p.tile >= p.end) {  // to the next segment that has a tile for this warp
+        while (p.next >= p.end) {  // to the next segment that has a tile for this warp
             if (p.rem == 0) {
                 p_live = false;
                 return;
@@ -238,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
             next_item(p);
             open(p);
         }
-        const int pg = page_of_tile(a, p.tile, &p_rest);
+        const int pg = page_of_tile(a, p.next, &p_rest);
         p_id = pg < a.b.width ? __ldg(a.b.table + p.b * a.b.stride + pg) : -1;
     };
     fetch_page();
@@ -252,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
             const uint32_t dst = ring_u + put * S::kStage;
             const bool ok = static_cast<uint32_t>(p_id) < static_cast<uint32_t>(a.c.pages);
             const int64_t r0 = int64_t(ok ? p_id : 0) * page_rows + (p.h * a.c.page + p_rest * kTile);
-            const int v0 = p.s.lo - p.tile * kTile, v1 = p.s.hi - p.tile * kTile;  // rows in use
+            const int v0 = p.lo - p.next * kTile, v1 = p.hi - p.next * kTile;  // rows in use
             if (ok && v0 <= 0 && v1 >= kTile) {
                 bad_mask &= ~(1u << put);
                 copy_tile<S, false>(dst, k_lane + r0 * S::kRow, v_lane + r0 * S::kRow, s_lane + r0, lane, 0, 0);
@@ -262,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 copy_tile<S, true>(dst, k_lane + r0 * S::kRow, v_lane + r0 * S::kRow, s_lane + r0, lane,
                                    ok ? v0 : kTile, v1);
             }
-            p.tile += kWarps;
+            p.next += kWarps;
             fetch_page();
         }
         put = put + 1 == S::kStages ? 0 : put + 1;
@@ -283,14 +305,14 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
         uint32_t bq[NT][S::kSteps][2];
         float f[NT][2], qsum[NT][2];  // scale * log2(e) without the row's power of two; sum of q
         int qpos[NT][2];  // position of the column's row
-        const int R = w.s.n * a.group;
+        const int r0 = w.tile * S::kTileRows, R = min(S::kTileRows, w.s.n * a.group - r0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = nt * 8 + g;
             const bool live = r < R;
-            const int i = r / a.group;
+            const int i = (r0 + r) / a.group;
             const uint16_t *qp = a.q + int64_t(w.s.row0 + i) * a.q_row +
-                                 (w.h * a.group + r - i * a.group) * a.q_head;
+                                 (w.h * a.group + r0 + r - i * a.group) * a.q_head;
             uint2 raw[S::kSteps];
             uint32_t top = 0;
 #pragma unroll
@@ -338,13 +360,13 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 qsum[nt][e] = FMT == W4KV_INT4 ? __shfl_sync(0xffffffffu, sum, 8 * c + 4 * e) : 0.f;
                 f[nt][e] = pow2i(-s2) * a.scale_log2;
                 const int rr = nt * 8 + 2 * c + e;
-                const int pos = w.s.first + rr / a.group;
+                const int pos = w.s.first + (r0 + rr) / a.group;
                 qpos[nt][e] = pos;
             }
         }
         // tiles inside [all_lo, all_hi) are seen whole by every row
-        const int all_hi = a.causal ? min(w.s.hi, w.s.first + 1) : w.s.hi;
-        const int all_lo = a.window > 0 ? max(w.s.lo, w.s.first + w.s.n - a.window) : w.s.lo;
+        const int all_hi = a.causal ? min(w.hi, w.s.first + r0 / a.group + 1) : w.hi;
+        const int all_lo = a.window > 0 ? max(w.lo, w.s.first + (r0 + R - 1) / a.group + 1 - a.window) : w.lo;
 
         float m[NT][2], l[NT][2], o[NT][S::kSteps][4];
 #pragma unroll
@@ -421,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
             bool grow = false, any_cut = false;
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
-                const int kv0 = (w.tile + n * kWarps) * kTile;
+                const int kv0 = (w.next + n * kWarps) * kTile;
                 const bool cut = bad[n] || kv0 < all_lo || kv0 + kTile > all_hi;  // warp-uniform
                 any_cut = any_cut || cut;
 #pragma unroll
@@ -442,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int j = kv0 + g + 8 * (i >> 1), pos = qpos[nt][i & 1];
-                            if (bad[n] || j < w.s.lo || j >= w.s.hi || (a.causal && j > pos) ||
+                            if (bad[n] || j < w.lo || j >= w.hi || (a.causal && j > pos) ||
                                 (a.window > 0 && j <= pos - a.window))
                                 sc[n][nt][i] = -INFINITY;
                         }
@@ -458,8 +480,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 for (int n = 0; n < NP; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int j = (w.tile + n * kWarps) * kTile + g + 8 * i;
-                        if (bad[n] || j < w.s.lo || j >= w.s.hi) vsw[n][i] = 0;
+                        const int j = (w.next + n * kWarps) * kTile + g + 8 * i;
+                        if (bad[n] || j < w.lo || j >= w.hi) vsw[n][i] = 0;
                     }
             }
             uint32_t ve = 0;
@@ -608,11 +630,11 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 }
             }
             get = get + NP < S::kStages ? get + NP : get + NP - S::kStages;
-            w.tile += NP * kWarps;
+            w.next += NP * kWarps;
         };
         if (S::kAtOnce == 2)
-            while (w.tile + kWarps < w.end) consume(std::integral_constant<int, 2>());
-        while (w.tile < w.end) consume(std::integral_constant<int, 1>());
+            while (w.next + kWarps < w.end) consume(std::integral_constant<int, 2>());
+        while (w.next < w.end) consume(std::integral_constant<int, 1>());
 
         // ---- the warps' results together ----
 #pragma unroll
@@ -654,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
         if (!whole && from_start && threadIdx.x == 0) {
             const int64_t last = range.end - w.rem + (w.nu - w.u1) - 1;  // its last unit
             a.desc[blockIdx.x] =
-                make_int4(w.b, w.h, block_of_unit(last, range) - static_cast<int>(blockIdx.x) + 1, 0);
+                make_int4(w.b, w.h, block_of_unit(last, range) - static_cast<int>(blockIdx.x) + 1, w.tile);
         }
         if (threadIdx.x < S::kTileRows) {
             const int r = threadIdx.x;
@@ -666,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 slot[r] = M;
                 slot[S::kTileRows + r] = L;
             } else if (a.lse && r < R) {
-                const int i = r / a.group;
-                a.lse[int64_t(w.s.row0 + i) * a.heads + w.h * a.group + r - i * a.group] =
+                const int i = (r0 + r) / a.group;
+                a.lse[int64_t(w.s.row0 + i) * a.heads + w.h * a.group + r0 + r - i * a.group] =
                     L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
             }
         }
@@ -704,9 +726,9 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 }
                 const int d = (D / 8) * (j & 7) + 2 * (ph * kT + (j >> 3));
                 if (whole) {
-                    const int t = r / a.group;
+                    const int t = (r0 + r) / a.group;
                     *reinterpret_cast<uint32_t *>(a.o + int64_t(w.s.row0 + t) * a.o_row +
-                                                  (w.h * a.group + r - t * a.group) * a.o_head + d) =
+                                                  (w.h * a.group + r0 + r - t * a.group) * a.o_head + d) =
                         narrow1<XT>(x) | static_cast<uint32_t>(narrow1<XT>(y)) << 16;
                 } else {
                     *reinterpret_cast<float2 *>(slot + 2 * S::kTileRows + r * D + d) = make_float2(x, y);
