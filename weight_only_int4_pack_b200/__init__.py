@@ -32,6 +32,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+import threading
 
 import torch
 
@@ -552,9 +554,9 @@ class W4KVCache:
         self.fmt, self.device = fmt, k_codes.device
         self.num_pages, self.kv_heads, self.page_size, row = k_codes.shape
         self.head_dim = 2 * row if fmt == W4KV_INT4 else row
-        self._c = _CCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                          v_scales.data_ptr(), self.num_pages, self.page_size, self.kv_heads,
-                          self.head_dim, fmt)
+        self._c = ctypes.pointer(_CCache(k_codes.data_ptr(), k_scales.data_ptr(),
+                                         v_codes.data_ptr(), v_scales.data_ptr(), self.num_pages,
+                                         self.page_size, self.kv_heads, self.head_dim, fmt))
 
 
 def w4kv_cache_empty(num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int,
@@ -566,20 +568,32 @@ def w4kv_cache_empty(num_pages: int, page_size: int, kv_heads: int, head_dim: in
                        ((shape + (row,), torch.uint8), (shape, torch.float32)) * 2), fmt)
 
 
+_kv_local = threading.local()  # one w4kv_batch per thread, filled anew for every call
+_kv_fill = struct.Struct("@PqqPPq").pack_into
+
+
 def _kv_batch(cache, page_table, kv_lens, cu_rows):
+    """Checks the batch and writes it into the thread's w4kv_batch; its address."""
     dev = cache.device
-    for t, name in ((page_table, "page_table"), (kv_lens, "kv_lens"), (cu_rows, "cu_rows")):
+    for t in (page_table, kv_lens, cu_rows):
         if t.dtype != torch.int32 or t.device != dev:
-            raise ValueError(f"{name} must be an int32 tensor on the cache's device")
-    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table, kv_lens and cu_rows must be int32 on the cache's device")
+    B, width = page_table.shape
+    stride, inner = page_table.stride()
+    if inner != 1 and width > 1:
         raise ValueError("page_table must be [batch][pages] with adjacent pages in a row")
-    B = page_table.shape[0]
     if kv_lens.shape != (B,) or cu_rows.shape != (B + 1,):
         raise ValueError("kv_lens must be [batch] and cu_rows [batch + 1]")
     if not (kv_lens.is_contiguous() and cu_rows.is_contiguous()):
         raise ValueError("kv_lens and cu_rows must be contiguous")
-    return _CBatch(page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-                   kv_lens.data_ptr(), cu_rows.data_ptr(), B)
+    try:
+        buf, ptr = _kv_local.batch
+    except AttributeError:
+        buf = ctypes.create_string_buffer(ctypes.sizeof(_CBatch))
+        ptr = ctypes.cast(buf, ctypes.POINTER(_CBatch))
+        _kv_local.batch = buf, ptr
+    _kv_fill(buf, 0, page_table.data_ptr(), stride, width, kv_lens.data_ptr(), cu_rows.data_ptr(), B)
+    return ptr
 
 
 def _kv_rows(t, cache, heads, name):
@@ -587,25 +601,30 @@ def _kv_rows(t, cache, heads, name):
         raise ValueError(f"{name} must live on the cache's device")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.head_dim:
         raise ValueError(f"{name} must be [rows][{heads}][{cache.head_dim}]")
-    if t.stride(2) != 1:
+    row, head, inner = t.stride()
+    if inner != 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent")
-    return t.stride(0), t.stride(1)
+    return row, head
 
 
-def _kv_call(fn, cache, stream, call, made=()):
-    """call(raw stream) with the cache's device current.  `made` are tensors
-    allocated for this call: on an explicit stream the allocator is told."""
-    dev = cache.device
-    if stream is not None:
-        for t in made:
-            t.record_stream(stream)
-    if dev.index == torch.cuda.current_device():
-        st = call(_stream(stream, dev.index))
+def _kv_call(name, cache, stream, fn, *args):
+    """fn(*args, raw stream) with the cache's device current."""
+    index = cache.device.index
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, _stream(stream, index))
     else:
-        with torch.cuda.device(dev):
-            st = call(_stream(stream, dev.index))
+        with torch.cuda.device(index):
+            st = fn(*args, _stream(stream, index))
     if st != W4_OK:
-        raise W4Error(fn, st)
+        raise W4Error(name, st)
+
+
+def _kv_made(stream, *tensors):
+    """Tells the allocator that an explicit stream uses tensors made for a call."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def w4kv_append(K, V, cache: W4KVCache, page_table, kv_lens, cu_rows, stream=None) -> None:
@@ -614,13 +633,11 @@ def w4kv_append(K, V, cache: W4KVCache, page_table, kv_lens, cu_rows, stream=Non
     sequence into the cache.  kv_lens counts them already."""
     if K.dtype != V.dtype or K.shape[0] != V.shape[0]:
         raise ValueError("K and V must share one dtype and their number of rows")
-    ks, vs = _kv_rows(K, cache, cache.kv_heads, "K"), _kv_rows(V, cache, cache.kv_heads, "V")
+    krs, khs = _kv_rows(K, cache, cache.kv_heads, "K")
+    vrs, vhs = _kv_rows(V, cache, cache.kv_heads, "V")
     b = _kv_batch(cache, page_table, kv_lens, cu_rows)
-    lib = _lib if _lib is not None else load()
-    dt = _dt(K)
-    _kv_call("w4kv_append", cache, stream,
-             lambda s: lib.w4kv_append(cache._c, b, K.data_ptr(), V.data_ptr(), dt, K.shape[0],
-                                       *ks, *vs, s))
+    _kv_call("w4kv_append", cache, stream, load().w4kv_append, cache._c, b, K.data_ptr(),
+             V.data_ptr(), _dt(K), K.shape[0], krs, khs, vrs, vhs)
 
 
 def w4kv_read(cache: W4KVCache, page_table, kv_lens, cu_rows, rows: int, dtype=torch.float16,
@@ -628,20 +645,20 @@ def w4kv_read(cache: W4KVCache, page_table, kv_lens, cu_rows, rows: int, dtype=t
     """The values of the last cu_rows[b + 1] - cu_rows[b] tokens of each
     sequence -> (K, V) [rows][kv_heads][head_dim]; `rows` is cu_rows[-1] (rows
     beyond it are left as they are).  `out` is an optional pair of tensors."""
-    made = ()
     if out is None:
-        made = out = tuple(torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=dtype,
-                                       device=cache.device) for _ in range(2))
-    K, V = out
-    if K.dtype != V.dtype or K.shape[0] != rows or V.shape[0] != rows:
-        raise ValueError("K and V must share one dtype and have `rows` rows")
-    ks, vs = _kv_rows(K, cache, cache.kv_heads, "K"), _kv_rows(V, cache, cache.kv_heads, "V")
+        shape = (rows, cache.kv_heads, cache.head_dim)
+        K = torch.empty(shape, dtype=dtype, device=cache.device)
+        V = torch.empty(shape, dtype=dtype, device=cache.device)
+        _kv_made(stream, K, V)
+    else:
+        K, V = out
+        if K.dtype != V.dtype or K.shape[0] != rows or V.shape[0] != rows:
+            raise ValueError("K and V must share one dtype and have `rows` rows")
+    krs, khs = _kv_rows(K, cache, cache.kv_heads, "K")
+    vrs, vhs = _kv_rows(V, cache, cache.kv_heads, "V")
     b = _kv_batch(cache, page_table, kv_lens, cu_rows)
-    lib = _lib if _lib is not None else load()
-    dt = _dt(K)
-    _kv_call("w4kv_read", cache, stream,
-             lambda s: lib.w4kv_read(cache._c, b, K.data_ptr(), V.data_ptr(), dt, rows, *ks, *vs, s),
-             made)
+    _kv_call("w4kv_read", cache, stream, load().w4kv_read, cache._c, b, K.data_ptr(), V.data_ptr(),
+             _dt(K), rows, krs, khs, vrs, vhs)
     return K, V
 
 
@@ -649,6 +666,9 @@ def w4kv_attention_workspace_bytes(cache: W4KVCache, batch: int, rows: int, max_
                                    heads: int) -> int:
     return int(load().w4kv_attention_workspace_bytes(cache._c, int(batch), int(rows),
                                                      int(max_rows), int(heads)))
+
+
+_kv_need = {}
 
 
 def w4kv_attention(Q, cache: W4KVCache, page_table, kv_lens, cu_rows, max_rows=None, scale=None,
@@ -665,38 +685,40 @@ def w4kv_attention(Q, cache: W4KVCache, page_table, kv_lens, cu_rows, max_rows=N
     `workspace` (uint8, w4kv_attention_workspace_bytes bytes, one per call in
     flight) is given."""
     rows, heads = Q.shape[0], Q.shape[1]
-    qs = _kv_rows(Q, cache, heads, "Q")
     dev = cache.device
-    O = out if out is not None else torch.empty((rows, heads, cache.head_dim), dtype=Q.dtype,
-                                                device=dev)
-    if O.dtype != Q.dtype or O.shape[0] != rows:
+    qrs, qhs = _kv_rows(Q, cache, heads, "Q")
+    O = out
+    if O is None:
+        O = torch.empty((rows, heads, cache.head_dim), dtype=Q.dtype, device=dev)
+    elif O.dtype != Q.dtype or O.shape[0] != rows:
         raise ValueError("out must have Q's dtype and rows")
-    os_ = _kv_rows(O, cache, heads, "out")
+    ors, ohs = _kv_rows(O, cache, heads, "out")
     lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
     b = _kv_batch(cache, page_table, kv_lens, cu_rows)
-    lib = _lib if _lib is not None else load()
-    if max_rows is None:
-        max_rows = max(rows, 1)
+    max_rows = max(rows, 1) if max_rows is None else int(max_rows)
     if scale is None:
         scale = cache.head_dim ** -0.5
-    dt = _dt(Q)
+    lib = load()
     ws = workspace
-    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
-        raise ValueError("workspace must be contiguous on the cache's device")
-    made = [t for t in (None if out is not None else O, lse) if t is not None]
-
-    def call(s):
-        nonlocal ws
-        if ws is None:
-            need = int(lib.w4kv_attention_workspace_bytes(cache._c, b.batch, rows, max_rows, heads))
-            if need:
-                ws = torch.empty(need, dtype=torch.uint8, device=dev)
-                if stream is not None:
-                    ws.record_stream(stream)
-        return lib.w4kv_attention(cache._c, b, Q.data_ptr(), dt, rows, heads, *qs, O.data_ptr(),
-                                  *os_, _p(lse), int(max_rows), float(scale), int(bool(causal)),
-                                  int(window), _p(ws),
-                                  0 if ws is None else ws.numel() * ws.element_size(), s)
-
-    _kv_call("w4kv_attention", cache, stream, call, made)
+    if ws is None:
+        # the size depends on the shapes and the device alone
+        key = (dev.index, cache.kv_heads, cache.head_dim, page_table.shape[0] > 1, rows, max_rows, heads)
+        need = _kv_need.get(key)
+        if need is None:
+            with torch.cuda.device(dev.index):
+                need = int(lib.w4kv_attention_workspace_bytes(cache._c, page_table.shape[0], rows,
+                                                              max_rows, heads))
+            _kv_need[key] = need
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        size = need
+    else:
+        if ws.device != dev or not ws.is_contiguous():
+            raise ValueError("workspace must be contiguous on the cache's device")
+        size = ws.numel() * ws.element_size()
+    if stream is not None:
+        _kv_made(stream, O if out is None else None, lse, ws if workspace is None else None)
+    _kv_call("w4kv_attention", cache, stream, lib.w4kv_attention, cache._c, b, Q.data_ptr(), _dt(Q),
+             rows, heads, qrs, qhs, O.data_ptr(), ors, ohs, None if lse is None else lse.data_ptr(),
+             max_rows, float(scale), int(bool(causal)), int(window),
+             None if ws is None else ws.data_ptr(), size)
     return (O, lse) if return_lse else O

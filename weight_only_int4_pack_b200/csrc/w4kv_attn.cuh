@@ -195,7 +195,7 @@ constexpr int kTiledRows = 256;
 int launch_tiled_attention(const Attn &a, int fmt, int dim, int xt, int grid, cudaStream_t stream);
 
 // Items of up to 16 (row, head) pairs: warp-level MMA (w4kv_attn_rows.cu).
-constexpr int rows_blocks_per_sm(int tile) { return tile == 8 ? 4 : 3; }
+constexpr int rows_blocks_per_sm(int tile) { return tile == 8 ? 4 : 2; }
 int launch_rows_attention(const Attn &a, int fmt, int dim, int xt, int tile, int grid,
                           cudaStream_t stream);
 

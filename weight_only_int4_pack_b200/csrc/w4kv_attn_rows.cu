@@ -54,7 +54,7 @@ struct Shape {
     static constexpr int kStage = 2 * kTile * kRow + 128;      // codes, then 32 scale words
     static constexpr int kBlocks = rows_blocks_per_sm(8 * NT);
     static constexpr int kAtOnce = 1;                // tiles that a warp takes at a time
-    static constexpr int kStages = kRow == 128 ? 3 : 5;
+    static constexpr int kStages = kRow == 128 ? (NT == 1 ? 3 : 5) : (NT == 1 ? 5 : 8);
     static constexpr int kSteps = D / 16;  // k steps of S, row tiles of O^T
     static constexpr int kTileRows = 8 * NT;
     static constexpr int kPhase = 32;  // dims joined at a time

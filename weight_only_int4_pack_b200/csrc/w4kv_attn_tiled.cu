@@ -504,14 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             // D / 8 lanes read a row together; lane i keeps the factor of row i of the warp.
             float fr = 1.f;
             {
-                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 32 / kAtOnce;
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;
                 const int part = lane % kLanes, sub = lane / kLanes;
                 uint8_t *qs = base + L::kQ + t * L::kTile + (part >> 3) * L::kBlock;
-                {
+#pragma unroll 1
+                for (int i = 0; i < 32; i += kBatch * kAtOnce) {
                     uint4 v[kBatch];
 #pragma unroll
                     for (int q = 0; q < kBatch; ++q) {  // all loads first
-                        const int lr = q * kAtOnce + sub, x = (row & ~31) + lr + (split ? 0 : t * kM);
+                        const int lr = i + q * kAtOnce + sub, x = (row & ~31) + lr + (split ? 0 : t * kM);
                         const int y = w.r0 + x, tok = y / a.group;
                         v[q] = x < w.R ? __ldg(reinterpret_cast<const uint4 *>(
                                                    a.q + int64_t(w.s.row0 + tok) * a.q_row +
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                     }
 #pragma unroll
                     for (int q = 0; q < kBatch; ++q) {
-                        const int lr = q * kAtOnce + sub;
+                        const int lr = i + q * kAtOnce + sub;
                         const uint32_t x = __vmaxu2(__vmaxu2(v[q].x & 0x7FFF7FFFu, v[q].y & 0x7FFF7FFFu),
                                                     __vmaxu2(v[q].z & 0x7FFF7FFFu, v[q].w & 0x7FFF7FFFu));
                         uint32_t top = max(x & 0xFFFFu, x >> 16);
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
 #pragma unroll
                         for (int o = 0; o < kAtOnce; ++o) {
                             const int s2 = __shfl_sync(0xffffffffu, sh, o * kLanes);
-                            if (lane == q * kAtOnce + o) fr = pow2i(-s2);
+                            if (lane == i + q * kAtOnce + o) fr = pow2i(-s2);
                         }
                     }
                 }
