@@ -18,34 +18,39 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kGroups = 4;  // row groups per warp, loaded together
+constexpr float kTinyScale = 0x1p-120f;  // below it a scale's reciprocal is out of range
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Codes of 8 consecutive elements x (of a row of LPR lanes) and the row's scale word.
-template <int FMT, int LPR>
-__device__ __forceinline__ uint2 encode8(const float x[8], uint32_t *word) {
-    uint32_t top = 0;  // largest |x| as bits: NaN > infinity > finite
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = LPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    bool bad = top >= 0x7F800000u;
+// Codes of 8 consecutive 16-bit elements w (of a row of LPR lanes) and the row's scale word.
+//
+// The row's extremes are found on the 16-bit patterns (non-negative floats order
+// like integers; NaN > infinity > finite), one shuffle per step.  Codes come from
+// the reciprocal: x * fl(1 / s) is within 3 * 2^-24 of fl(x / s), relatively, so a
+// code is the exact one unless the quotient lies that near a rounding border; a
+// lane that holds such a one, and a scale whose reciprocal is out of range, takes
+// the IEEE division.
+template <int FMT, int LPR, int XT>
+__device__ __forceinline__ uint2 encode8(const uint4 w, uint32_t *word) {
+    constexpr uint32_t kInf = XT == W4_F16 ? 0x7C00u : 0x7F80u;
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
+    float x[8];
+    widen8<XT>(w, x);
     if (FMT == W4KV_INT4) {
-        float lo = 0.f, hi = 0.f;
+        // the largest element, and the largest of the negated ones, at least 0
+        uint32_t p = __vmaxs2(__vmaxs2(w.x, w.y), __vmaxs2(w.z, w.w));
+        uint32_t q = __vmaxs2(__vmaxs2(w.x ^ 0x80008000u, w.y ^ 0x80008000u),
+                              __vmaxs2(w.z ^ 0x80008000u, w.w ^ 0x80008000u));
+        uint32_t pq = __vmaxs2(__vmaxs2(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632)), 0u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo = fminf(lo, x[i]);
-            hi = fmaxf(hi, x[i]);
-        }
-#pragma unroll
-        for (int o = LPR / 2; o; o >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
+        for (int o = LPR / 2; o; o >>= 1) pq = __vmaxu2(pq, __shfl_xor_sync(0xffffffffu, pq, o));
+        const float hi = widen1<XT>(static_cast<uint16_t>(pq & 0xFFFFu));
+        const float lo = -widen1<XT>(static_cast<uint16_t>(pq >> 16));
         const float range = __fsub_rn(hi, lo);
-        bad = bad || __float_as_uint(range) >= 0x7F800000u;
+        const bool bad = (pq & 0xFFFFu) >= kInf || (pq >> 16) >= kInf ||
+                         __float_as_uint(range) >= 0x7F800000u;
         const uint32_t sb = (__float_as_uint(__fdiv_rn(range, 15.f)) + 8u) & ~15u;
         if (bad || sb == 0) {
             *word = bad ? 0x7FC00000u : 0u;
@@ -54,36 +59,72 @@ __device__ __forceinline__ uint2 encode8(const float x[8], uint32_t *word) {
         const float s = __uint_as_float(sb);
         const float z = rintf(__fdiv_rn(-lo, s));
         *word = sb | static_cast<uint32_t>(z);
+        const float r = __frcp_rn(s);
+        bool near = s < kTinyScale;
+        uint32_t c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // 0 <= code by the choice of z; 15.5 rounds to 16
+            const float v = fminf(fmaf(x[i], r, z), 15.f), m = v + kMagic;
+            near = near || fabsf(v - (m - kMagic)) > 0.5f - 0x1p-18f;  // 3 * 2^-24 * 16 < 2^-18
+            c[i] = __float_as_uint(m);
+        }
+        if (near) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                c[i] = static_cast<uint32_t>(
+                    fminf(fmaxf(rintf(__fadd_rn(__fdiv_rn(x[i], s), z)), 0.f), 15.f));
+        }
+        // nibble of element i in the little-endian word: 0,4,1,5,2,6,3,7
         uint32_t u = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float c = fminf(fmaxf(rintf(__fadd_rn(__fdiv_rn(x[i], s), z)), 0.f), 15.f);
-            // nibble of element i in the little-endian word: 0,4,1,5,2,6,3,7
-            u |= static_cast<uint32_t>(c) << (4 * ((i >> 1) + 4 * (i & 1)));
-        }
+        for (int i = 0; i < 8; ++i) u |= (c[i] & 15u) << (4 * ((i >> 1) + 4 * (i & 1)));
         return make_uint2(u, 0);
     }
-    const float s = __fdiv_rn(__uint_as_float(top), FMT == W4KV_INT8 ? 127.f : 448.f);
+    uint32_t t = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                          __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+    const uint32_t top = max(t & 0xFFFFu, t >> 16);
+    const bool bad = top >= kInf;
+    const float s = __fdiv_rn(widen1<XT>(static_cast<uint16_t>(top)), FMT == W4KV_INT8 ? 127.f : 448.f);
     if (bad || s == 0.f) {
         *word = bad ? 0x7FC00000u : 0u;
         return make_uint2(0, 0);
     }
     *word = __float_as_uint(s);
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+    const float rc = __frcp_rn(s);
+    bool near = s < kTinyScale;
     uint2 r;
     if (FMT == W4KV_INT8) {
-        uint32_t b[8];
+        uint32_t c[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            b[i] = static_cast<uint32_t>(
-                       static_cast<int>(fminf(fmaxf(rintf(y[i]), -127.f), 127.f))) & 0xFFu;
-        r.x = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
-        r.y = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
+        for (int i = 0; i < 8; ++i) {  // |x| <= amax: no code beyond 127
+            const float v = x[i] * rc, m = v + kMagic;
+            near = near || fabsf(v - (m - kMagic)) > 0.5f - 0x1p-15f;  // 3 * 2^-24 * 127 < 2^-15
+            c[i] = __float_as_uint(m);
+        }
+        if (near) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                c[i] = static_cast<uint32_t>(static_cast<int>(
+                    fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -127.f), 127.f)));
+        }
+        r.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        r.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
     } else {
-        r.x = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
-        r.y = e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16;
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // a code is exact where both ends of the error agree
+            const float v0 = x[2 * i] * rc, v1 = x[2 * i + 1] * rc;
+            c[i] = e4m3x2(v0 * (1.f - 0x1p-22f), v1 * (1.f - 0x1p-22f));
+            near = near || c[i] != e4m3x2(v0 * (1.f + 0x1p-22f), v1 * (1.f + 0x1p-22f));
+        }
+        if (near) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = e4m3x2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
+        }
+        r.x = c[0] | c[1] << 16;
+        r.y = c[2] | c[3] << 16;
     }
     return r;
 }
@@ -172,9 +213,9 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Cache c, const Bat
     for (int g = 0; g < kGroups; ++g) {
         const int u = (g0 + g) * kRpw + lane / kLpr;
         const int kv = u >= c.heads, h = u - kv * c.heads;
-        float f[8];
         if (READ) {
             if (u >= n) continue;
+            float f[8];
             decode8<FMT>(code[g], word[g], f);
             uint32_t o[4];
 #pragma unroll
@@ -184,14 +225,9 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Cache c, const Bat
                 make_uint4(o[0], o[1], o[2], o[3]);
         } else {
             // every lane takes part in the row reductions; idle ones carry zeros
-            if (u < n) {
-                widen8<XT>(w16[g], f);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = 0.f;
-            }
+            if (u >= n) w16[g] = make_uint4(0, 0, 0, 0);
             uint32_t sw;
-            const uint2 cd = encode8<FMT, kLpr>(f, &sw);
+            const uint2 cd = encode8<FMT, kLpr, XT>(w16[g], &sw);
             if (u >= n) continue;
             const int64_t r = row0 + int64_t(h) * c.page;
             uint8_t *p = (kv ? c.v : c.k) + r * c.row_bytes + (e / 8) * kCode;
