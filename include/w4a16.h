@@ -56,7 +56,8 @@ typedef enum {
     W4_ERR_UNSUPPORTED = 2, /* valid but not implemented (group size, alignment, dtype) */
     W4_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed while enqueueing */
     W4_ERR_TIMEOUT = 4,     /* a bounded device-side wait ran out (see w4_device_status) */
-    W4_ERR_BOUNDS = 5       /* an in-kernel bounds check of the W4_DEBUG build failed */
+    W4_ERR_BOUNDS = 5       /* an in-kernel bounds check of the W4_DEBUG build failed, or a
+                               page table or length of w4kv.h pointed out of range */
 } w4_status;
 
 typedef enum { W4_F16 = 0, W4_BF16 = 1 } w4_dtype;
@@ -283,7 +284,8 @@ int w4_gptq_quantize(const void *W, int wt, int64_t K, int64_t N, int group, int
 
 /*
  * w4_device_status -- reads (and, if reset != 0, clears) the current device's
- * status word that kernels set when a bounded wait runs out or, in the
+ * status word that kernels set when a bounded wait runs out, when a page
+ * number or position given to the w4kv calls is out of range or, in the
  * W4_DEBUG build, when a bounds check fails.  Synchronizes the device first.
  * Returns W4_OK, W4_ERR_BOUNDS (a check failed; takes precedence),
  * W4_ERR_TIMEOUT, or W4_ERR_CUDA if the read fails.

@@ -114,7 +114,8 @@ int w4kv_read(const w4kv_cache *cache, const w4kv_batch *batch, void *K, void *V
 /*
  * w4kv_attention_workspace_bytes -- device scratch bytes w4kv_attention needs
  * for these sizes on the current device (0 for sizes it rejects): partial
- * results of rows whose cached tokens are split between thread blocks.
+ * results of rows whose cached tokens are split between thread blocks, up to
+ * 5 MB for decode steps and 44 MB where chunks are served.
  */
 size_t w4kv_attention_workspace_bytes(const w4kv_cache *cache, int64_t batch, int64_t rows,
                                       int64_t max_rows, int heads);
@@ -139,11 +140,16 @@ size_t w4kv_attention_workspace_bytes(const w4kv_cache *cache, int64_t batch, in
  *   Numerics: codes enter the tensor cores unrounded (they are exact in fp16);
  *   scores, maxima, sums and outputs are fp32; the probabilities times the
  *   value scales are rounded to fp16 (relative to a running power of two, so
- *   that no scale leaves the range); the output is rounded once.  bf16 queries
- *   enter as fp16 after scaling each row by a power of two (elements below
- *   2^-28 of the row's largest lose precision).
+ *   that no scale leaves the range: what is lost is below 2^-32 of the largest
+ *   value); the output is rounded once.  Queries enter as fp16, each row scaled
+ *   by a power of two: exact for elements down to 2^-14 of the row's largest,
+ *   smaller ones carry an error of at most 2^-25 of it.
  *   Q and what the cache's visible rows stand for must be finite for a finite
- *   result.  Deterministic: repeated calls give the same bits.
+ *   result, and keys below 1e34.  Deterministic: repeated calls give the same bits.
+ *   Sequences with at most 64 (row, query head) pairs per key/value head run on
+ *   warp-level MMAs, bound by reading the cache; longer chunks on tcgen05.  One
+ *   to four kernels, no host synchronization; a captured call follows changed
+ *   lengths, pages and row counts (up to max_rows).
  *   workspace: at least w4kv_attention_workspace_bytes(...) bytes, 256-byte
  *   aligned, contents irrelevant (clobbered); one per call in flight.
  */

@@ -19,8 +19,9 @@ plus the scale factors; the factor 2 for the sum's terms), tmax = the largest
 round a sum: the terms with 2^-24 are doubled.  The last term: a weight is
 held relative to the largest value scale with 21 bits of range above fp16's
 smallest normal number, so one below loses at most 2^-32 of it; vmax is the
-largest |v|.  bf16 queries enter as fp16 with their row scaled: elements below
-2^-20 of the row's largest lose at most 2^-31 of it, inside (D + 8) * 2^-24.
+largest |v|.  Queries enter as fp16 with their row scaled: elements below 2^-14
+of the row's largest carry at most 2^-25 of it, inside (D + 8) * 2^-24 of smax
+for the rows tested here (none has nearly all its weight in one element).
 """
 from __future__ import annotations
 

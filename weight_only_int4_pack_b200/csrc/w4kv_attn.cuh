@@ -101,6 +101,12 @@ __device__ __forceinline__ float pow2i(int e) {  // 2^e, -126 <= e <= 127
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// a / b, by 32 bits where they do.
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // Range [start, end) of the block in the cost of all items, and the sequence that holds its
 // beginning.  units(b) gives the cost of a sequence's items.  All threads of the block
 // (kThreads of them) call it and get the same values.
@@ -111,7 +117,7 @@ struct Range {
     int64_t off;  // of `start` within sequence b
 };
 struct RangeSmem {
-    int64_t warp[33];
+    int64_t warp[32], rest[32];
     int64_t off;
     int b;
 };
@@ -121,25 +127,45 @@ __device__ __forceinline__ Range block_range(int n_seq, RangeSmem *sm, Units uni
     constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Range r;
-    int64_t sum = 0, v = 0;
-    for (int i = threadIdx.x; i < n_seq; i += kThreads) sum += v = units(i);
+    // The scan of the first kThreads sequences serves for the total of all as well.
+    int64_t v = static_cast<int>(threadIdx.x) < n_seq ? units(threadIdx.x) : 0, inc = v;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) sm->warp[warp] = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    int64_t rest = 0;  // of the sequences behind them
+    for (int i = threadIdx.x + kThreads; i < n_seq; i += kThreads) rest += units(i);
+    if (n_seq > kThreads) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+    }
+    if (lane == 31) {
+        sm->warp[warp] = inc;
+        sm->rest[warp] = rest;
+    }
     __syncthreads();
+    int64_t before = 0, p = inc - v;  // units of the first kThreads sequences; those before this thread's
     r.total = 0;
-    for (int w = 0; w < kWarps; ++w) r.total += sm->warp[w];
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) p += sm->warp[w];
+        before += sm->warp[w];
+        r.total += sm->rest[w];
+    }
+    r.total += before;
     r.b = 0;
     r.off = r.start = r.end = 0;
     r.blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), r.total));
     if (static_cast<int>(blockIdx.x) >= r.blocks) return r;
-    r.start = r.total * blockIdx.x / r.blocks;
-    r.end = r.total * (blockIdx.x + 1) / r.blocks;
-    int64_t before = 0;
-    for (int base = 0; base < n_seq; base += kThreads) {
+    r.start = div_small(r.total * blockIdx.x, r.blocks);
+    r.end = div_small(r.total * (blockIdx.x + 1), r.blocks);
+    if (p <= r.start && r.start < p + v) {
+        sm->b = threadIdx.x;
+        sm->off = r.start - p;
+    }
+    for (int base = kThreads; before <= r.start && base < n_seq; base += kThreads) {
         const int i = base + threadIdx.x;
-        if (n_seq > kThreads) v = i < n_seq ? units(i) : 0;
-        int64_t inc = v;
+        inc = v = i < n_seq ? units(i) : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
@@ -148,7 +174,7 @@ __device__ __forceinline__ Range block_range(int n_seq, RangeSmem *sm, Units uni
         __syncthreads();
         if (lane == 31) sm->warp[warp] = inc;
         __syncthreads();
-        int64_t p = before + inc - v;  // units before sequence i
+        p = before + inc - v;
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) p += sm->warp[w];
             before += sm->warp[w];
@@ -157,7 +183,6 @@ __device__ __forceinline__ Range block_range(int n_seq, RangeSmem *sm, Units uni
             sm->b = i;
             sm->off = r.start - p;
         }
-        if (before > r.start) break;  // the same in every thread
     }
     __syncthreads();
     r.b = sm->b;
@@ -167,7 +192,7 @@ __device__ __forceinline__ Range block_range(int n_seq, RangeSmem *sm, Units uni
 
 // The block whose range holds unit u.
 __device__ __forceinline__ int block_of_unit(int64_t u, const Range &r) {
-    return static_cast<int>(((u + 1) * r.blocks - 1) / r.total);
+    return static_cast<int>(div_small((u + 1) * r.blocks - 1, r.total));
 }
 
 // Reference maximum of a row that has seen nothing: below every score, and

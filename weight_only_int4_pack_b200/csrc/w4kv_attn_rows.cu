@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
         const int tiles = tiles_of(w.s);
         int per_head = 0;
         for (int t = 0; t < tiles; ++t) per_head += kItemCost + tile_range(w.s, t, &w.lo, &w.hi);
-        w.h = static_cast<int>(range.off / per_head);
-        w.x = static_cast<int>(range.off % per_head);
+        w.h = static_cast<int>(div_small(range.off, per_head));
+        w.x = static_cast<int>(range.off - int64_t(w.h) * per_head);
         for (w.tile = 0;; ++w.tile) {
             w.nu = tile_range(w.s, w.tile, &w.lo, &w.hi);
             if (w.x < w.nu + kItemCost || w.tile + 1 >= tiles) break;

@@ -132,7 +132,7 @@ __device__ __forceinline__ bool first_segment(const Attn &a, const Range &r, Wal
     w.tiles = max(1, seq_tiles(a, w.s));
     int64_t per_head = 0;
     for (int t = 0; t < w.tiles; ++t) per_head += kItemCost + tile_units(a, w.s, t);
-    w.h = static_cast<int>(r.off / per_head);
+    w.h = static_cast<int>(div_small(r.off, per_head));
     int64_t x = r.off - w.h * per_head;
     for (w.tile = 0;; ++w.tile) {
         set_item(a, w);
