@@ -5,11 +5,10 @@
 // Mathematics: one pass over the cache with a running maximum m, sum l and
 // output O per row; a score is q . codes times the key row's scale, a weight
 // is p = 2^(score - m) times the value row's scale.  The codes enter the MMAs
-// exactly (INT8 and E4M3 are fp16 numbers, and so are an INT4 value's u - z and
-// 16 (u - z); an INT4 key enters as the fp16 subnormals u * 2^-24, with
-// q . (u - z) = q . u - z sum q.  For the values that form is too coarse: the
-// MMA aligns a subnormal as if it were 2^-14, which leaves an error of 2^-14 of
-// the largest weight where u - z is 0).  m moves only when a score exceeds it by
+// exactly: INT8 and E4M3 are fp16 numbers, and so are u - z and 16 (u - z) of
+// INT4, which saves half of the shifts.  (The fp16 subnormals u * 2^-24, with the
+// zero points taken off the sums, would save the subtraction, but the MMA aligns
+// them as if they were 2^-14: errors of 2^-14 of the largest product.)  m moves only when a score exceeds it by
 // 2^8, so that O is rarely rescaled; p <= 2^8 then, and the value scales are
 // taken relative to 2^k > their running maximum / 2^7, so that a weight fits
 // fp16 (below 2^15) with 21 bits of range under the largest one.
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
         }
         // ---- the item's query rows as B fragments, and what each column sees ----
         uint32_t bq[NT][S::kSteps][2];
-        float f[NT][2], qsum[NT][2];  // scale * log2(e) without the row's power of two; sum of q
+        float f[NT][2];  // scale * log2(e) without the row's power of two
         int qpos[NT][2];  // position of the column's row
         const int r0 = w.tile * S::kTileRows, R = min(S::kTileRows, w.s.n * a.group - r0);
 #pragma unroll
@@ -332,32 +331,22 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 if (t32 != 0 && t32 < 0x7F800000u) sh = min(120, 131 - static_cast<int>(t32 >> 23));
             }
             const float up = pow2i(sh);
-            float sum = 0.f;
 #pragma unroll
             for (int s = 0; s < S::kSteps; ++s) {
                 const float e0 = widen1<XT>(raw[s].x & 0xFFFF) * up, e1 = widen1<XT>(raw[s].x >> 16) * up;
                 float e2 = widen1<XT>(raw[s].y & 0xFFFF) * up, e3 = widen1<XT>(raw[s].y >> 16) * up;
-                if (FMT == W4KV_INT4) {  // the second pair's codes stand 4 bits higher
+                if (FMT == W4KV_INT4) {  // the second pair's codes come 16-fold
                     e2 *= 0.0625f;
                     e3 *= 0.0625f;
                 }
                 const __half2 h0 = __floats2half2_rn(e0, e1), h1 = __floats2half2_rn(e2, e3);
-                if (FMT == W4KV_INT4) {
-                    const float2 x = __half22float2(h0), y = __half22float2(h1);
-                    sum += (x.x + x.y) + 16.f * (y.x + y.y);
-                }
                 bq[nt][s][0] = *reinterpret_cast<const uint32_t *>(&h0);
                 bq[nt][s][1] = *reinterpret_cast<const uint32_t *>(&h1);
-            }
-            if (FMT == W4KV_INT4) {
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             }
             // this lane's score columns are 2c, 2c + 1: their rows' values live in lanes 8c, 8c + 4
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int s2 = __shfl_sync(0xffffffffu, sh, 8 * c + 4 * e);
-                qsum[nt][e] = FMT == W4KV_INT4 ? __shfl_sync(0xffffffffu, sum, 8 * c + 4 * e) : 0.f;
                 f[nt][e] = pow2i(-s2) * a.scale_log2;
                 const int rr = nt * 8 + 2 * c + e;
                 const int pos = w.s.first + (r0 + rr) / a.group;
@@ -427,11 +416,16 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
 #pragma unroll
                 for (int n = 0; n < NP; ++n) {
                     uint32_t fa[4];
-                    if (FMT == W4KV_INT4) {  // nibbles as subnormals u * 2^-24, or 16 u * 2^-24
-                        const uint32_t x = kw[n][0][s >> 1] >> (8 * (s & 1));
-                        const uint32_t y = kw[n][1][s >> 1] >> (8 * (s & 1));
-                        fa[0] = x & 0x000F000Fu, fa[2] = x & 0x00F000F0u;
-                        fa[1] = y & 0x000F000Fu, fa[3] = y & 0x00F000F0u;
+                    if (FMT == W4KV_INT4) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {  // u - z, then 16 (u - z), of rows g, g + 8
+                            const uint32_t x = kw[n][q & 1][s >> 1] >> (8 * (s & 1));
+                            const uint32_t u = (x & (q & 2 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+                            const uint32_t z = (ksw[n][q & 1] & 15u) * (q & 2 ? 0x100010u : 0x10001u) | 0x64006400u;
+                            const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u),
+                                                      *reinterpret_cast<const __half2 *>(&z));
+                            fa[q] = *reinterpret_cast<const uint32_t *>(&r);
+                        }
                     } else {
                         widen4<FMT>(kw[n][0][s], &fa[0], &fa[2]);
                         widen4<FMT>(kw[n][1][s], &fa[1], &fa[3]);
@@ -453,8 +447,6 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                         const int e = i & 1;
                         const uint32_t kw_ = ksw[n][i >> 1];
                         float x = sc[n][nt][i];
-                        if (FMT == W4KV_INT4)
-                            x = fmaf(x, 16777216.f, -static_cast<float>(kw_ & 15u) * qsum[nt][e]);
                         x *= FMT == W4KV_INT4 ? int4_scale(kw_) : __uint_as_float(kw_);
                         sc[n][nt][i] = x * f[nt][e];
                     }
@@ -523,7 +515,10 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
             }
             const float vmul = pow2i(133 - vexp);
             // ---- weights, transposed into B fragments ----
-            uint32_t pb[NP][NT][2];
+            // For fp16 outputs a weight is fed as the sum of two fp16 numbers: one alone would
+            // err as much as the output's own rounding (0.0003 instead of 0.0002 in all).
+            constexpr int kParts = XT == W4_F16 ? 2 : 1;
+            uint32_t pb[kParts][NP][NT][2];
 #pragma unroll
             for (int n = 0; n < NP; ++n)
 #pragma unroll
@@ -542,8 +537,13 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                             // unseen: exactly zero, whatever the value row's scale is
                             if (any_cut && x == -INFINITY) pw[e] = 0.f;
                         }
-                        const __half2 h = __floats2half2_rn(pw[0], pw[1]);
-                        pb[n][nt][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
+                        __half2 h = __floats2half2_rn(pw[0], pw[1]);
+                        pb[0][n][nt][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
+                        if (kParts == 2) {
+                            const float2 r = __half22float2(h);
+                            h = __floats2half2_rn(pw[0] - r.x, pw[1] - r.y);
+                            pb[kParts - 1][n][nt][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
+                        }
                     }
                 }
             // ---- O^T += V^T P^T ----
@@ -607,7 +607,9 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                             }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma(o[nt][4 * j + t], fa, pb[n][nt][0], pb[n][nt][1]);
+#pragma unroll
+                                for (int q = 0; q < kParts; ++q)
+                                    mma(o[nt][4 * j + t], fa, pb[q][n][nt][0], pb[q][n][nt][1]);
                         }
                     }
                 } else {
@@ -625,7 +627,9 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                         for (int t = 0; t < 2; ++t)
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma(o[nt][2 * j + t], fa[t], pb[n][nt][0], pb[n][nt][1]);
+#pragma unroll
+                                for (int q = 0; q < kParts; ++q)
+                                    mma(o[nt][2 * j + t], fa[t], pb[q][n][nt][0], pb[q][n][nt][1]);
                     }
                 }
             }
