@@ -600,3 +600,35 @@ def test_offsets_beyond_32_bits(w4):
         O = w4.w4kv_attention(Q.cuda(), cache, table, lens,
                               torch.tensor([0, m], dtype=torch.int32, device="cuda"))
         close(O, None, R.attention(p, Q, [m], D ** -0.5))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_attention_random_calls(w4, seed):
+    """Calls drawn over formats, types, layouts, lengths, masks and row counts."""
+    r = np.random.default_rng(1000 + seed)
+    fmt, D = int(r.integers(3)), int(r.choice([64, 128]))
+    Hk, G = int(r.integers(1, 4)), int(r.choice([1, 2, 3, 5, 8, 11]))
+    B = int(r.integers(1, 7))
+    n_rows = [int(r.choice([0, 1, 1, 2, 7, 20, 90, 140])) for _ in range(B)]
+    lens = [max(1, n + int(r.integers(-3, 500))) for n in n_rows]
+    if sum(n_rows) == 0:
+        n_rows[0] = 1
+    causal = bool(r.random() < 0.8)
+    window = int(r.integers(1, 300)) if causal and r.random() < 0.4 else 0
+    dtype = DTYPES[int(r.integers(2))]
+    p = R.Plain(lens, fmt, Hk, D, int(r.choice([16, 48, 64, 128])), seed, dtype=dtype)
+    check_attention(w4, p, n_rows, Hk * G, dtype, seed, causal, window,
+                    scale=float(r.choice([D ** -0.5, 0.02, 0.3])), q_scale=float(r.choice([1.0, 4.0])),
+                    max_rows=max(n_rows) + int(r.integers(0, 100)))
+
+
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_attention_errors_are_small(w4, fmt):
+    """fp16 decode steps: the error's norm is the output rounding's (2^-11 / sqrt 3
+    of a value at most), to 1.3; chunks carry the weights' rounding too, to 1.8."""
+    p = R.Plain([700, 300], fmt, 2, 128, 16, 5)
+    for n_rows, limit in (([1, 1], 1.3), ([5, 4], 1.3), ([90, 70], 1.8)):
+        Q = rows((sum(n_rows), 8, 128), torch.float16, 4)
+        O = w4.w4kv_attention(Q.cuda(), p.device(w4), *p.batch(n_rows)).cpu().double()
+        want = R.attention(p, Q, n_rows, 128 ** -0.5)[0]
+        assert (O - want).norm() <= limit * 2.0 ** -11 / 3 ** 0.5 * want.norm()
