@@ -60,6 +60,18 @@ __global__ void __launch_bounds__(256) combine_kernel(const Attn a, int tile, in
 
 }  // namespace
 
+int allow_smem(const void *kernel, int bytes, std::atomic<unsigned long long> *ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail("cudaGetDevice", e);
+    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (ready->load(std::memory_order_acquire) & bit) return W4_OK;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(attention kernel)", e);
+    ready->fetch_or(bit, std::memory_order_release);
+    return W4_OK;
+}
+
 int launch_combine(const Attn &a, int grid, int tile, int dim, int xt, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, max(1, tile * dim / 4 / 1024));

@@ -13,6 +13,8 @@
 // over the sequences, then a scan of the 256 that hold its first unit.
 #pragma once
 
+#include <atomic>
+
 #include "w4kv.cuh"
 
 namespace w4 {
@@ -210,6 +212,9 @@ inline uint32_t page_magic(int page) {
     const uint32_t d = static_cast<uint32_t>(page) >> 4;
     return d == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((uint64_t(1) << 32) / d);
 }
+
+// Lets a kernel use `bytes` of dynamic shared memory; once per device.
+int allow_smem(const void *kernel, int bytes, std::atomic<unsigned long long> *ready);
 
 // Joins the partial results of items that several blocks share; after each
 // attention kernel, with that kernel's grid and `tile` rows per slot.

@@ -751,8 +751,9 @@ template <int FMT, int D, int XT, int NT>
 int run(const Attn &a, int grid, cudaStream_t stream) {
     using S = Shape<FMT, D, NT>;
     auto kernel = rows_kernel<FMT, D, XT, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(rows_kernel)", e);
+    static std::atomic<unsigned long long> ready{0};  // a bit per device
+    const int st = allow_smem(reinterpret_cast<const void *>(kernel), S::kSmem, &ready);
+    if (st != W4_OK) return st;
     kernel<<<grid, kThreads, S::kSmem, stream>>>(a);
     return cuda_status(cudaGetLastError());
 }

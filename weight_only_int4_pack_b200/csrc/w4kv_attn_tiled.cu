@@ -1159,8 +1159,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
 template <int FMT, int D, int XT>
 int run(const Attn &a, int grid, cudaStream_t stream) {
     auto kernel = tiled_kernel<FMT, D, XT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<FMT, D>::kSmem);
-    if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(tiled_kernel)", e);
+    static std::atomic<unsigned long long> ready{0};  // a bit per device
+    const int st = allow_smem(reinterpret_cast<const void *>(kernel), Layout<FMT, D>::kSmem, &ready);
+    if (st != W4_OK) return st;
     kernel<<<grid, kThreads, Layout<FMT, D>::kSmem, stream>>>(a);
     return cuda_status(cudaGetLastError());
 }
