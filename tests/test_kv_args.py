@@ -56,7 +56,8 @@ BAD_CACHE = [(dict(fmt=3), 1), (dict(fmt=-1), 1), (dict(num_pages=0), 1), (dict(
              (dict(kv_heads=0), 1), (dict(page_size=0), 1), (dict(head_dim=0), 1),
              (dict(k_codes=None), 1), (dict(v_codes=None), 1), (dict(k_scales=None), 1),
              (dict(v_scales=None), 1), (dict(page_size=8), 2), (dict(page_size=24), 2),
-             (dict(page_size=1 << 17), 2), (dict(head_dim=96), 2), (dict(head_dim=256), 2),
+             (dict(page_size=1 << 17), 2),
+             (dict(page_size=1 << 16, kv_heads=1 << 15), 2), (dict(head_dim=96), 2), (dict(head_dim=256), 2),
              (dict(k_codes=0x100008), 2), (dict(v_scales=0x400004), 2)]
 BAD_BATCH = [(dict(batch=-1), 1), (dict(batch=(1 << 20) + 1), 1), (dict(page_table=None), 1),
              (dict(kv_lens=None), 1), (dict(cu_rows=None), 1), (dict(table_width=0), 1),
@@ -124,6 +125,7 @@ def test_overlapping_outputs(lib, kw):
     (dict(window=4, causal=0), 1), (dict(Q=None), 1), (dict(O=None), 1), (dict(ohs=64), 1),
     (dict(ors=512), 1), (dict(O=0x900008), 2), (dict(qrs=1028), 2), (dict(lse=0x2), 2),
     (dict(rows=0, Q=None, O=None), 0),
+    (dict(rows=1 << 29, max_rows=1 << 29, qrs=1024, ors=1024), 1),   # rows * heads / kv_heads
 ])
 def test_bad_attention(lib, kw, status):
     assert attn_call(lib, **kw) == status

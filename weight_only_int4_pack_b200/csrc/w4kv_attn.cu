@@ -168,11 +168,11 @@ int w4kv_attention(const w4kv_cache *cache, const w4kv_batch *batch, const void 
     if ((st = check_rows(fn, O, rows, heads, D, o_row_stride, o_head_stride, true)) != W4_OK) return st;
     if (reinterpret_cast<uintptr_t>(lse) & 3u)
         return set_error(W4_ERR_UNSUPPORTED, fn, "lse must be 4-byte aligned");
-    DeviceInfo d;
-    if ((st = device_info(&d)) != W4_OK) return st;
     if (max_rows > rows) max_rows = rows;
     if (max_rows * (heads / a.c.heads) > 0x7FFFFFFF - kTiledRows)
         return set_error(W4_ERR_INVALID_ARG, fn, "max_rows * heads / kv_heads too large");
+    DeviceInfo d;
+    if ((st = device_info(&d)) != W4_OK) return st;
     const Plan p = make_plan(d, D, a.b.n, max_rows, heads / a.c.heads);
     if (p.total > 0 && (!workspace || workspace_bytes < p.total ||
                         (reinterpret_cast<uintptr_t>(workspace) & 255u)))

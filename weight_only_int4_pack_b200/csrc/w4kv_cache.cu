@@ -305,6 +305,8 @@ int check_cache(const char *fn, const w4kv_cache *c, Cache *out) {
         return set_error(W4_ERR_INVALID_ARG, fn, "null pointer in the cache");
     if (c->page_size % 16 != 0 || c->page_size > 65536)
         return set_error(W4_ERR_UNSUPPORTED, fn, "page_size must be a multiple of 16 up to 65536");
+    if (int64_t(c->kv_heads) * c->page_size > 0x7FFFFFFF)
+        return set_error(W4_ERR_UNSUPPORTED, fn, "kv_heads * page_size must be below 2^31");
     if (c->head_dim != 64 && c->head_dim != 128)
         return set_error(W4_ERR_UNSUPPORTED, fn, "head_dim must be 64 or 128");
     if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) ||
