@@ -28,9 +28,15 @@
 //   * value fragments pair two tokens of one dim: bytes of two rows'
 //     words, merged with byte permutations.
 //   * P^T needs one 8x8 transpose per 8 tokens (movmatrix).
-// A block of 8 warps takes an item's 16-token tiles round robin (two at a
-// time per warp, for two independent MMA chains), joins its warps' results in
-// shared memory at the item's end, and prefetches across items.
+// A block of 4 warps takes an item's 16-token tiles round robin, joins its warps'
+// results in shared memory at the item's end, and prefetches across items; 16
+// warps an SM (8 with tiles of 16 query rows) hide the chain of a tile.
+//
+// Measured: 64 sequences to 16384 tokens, 64 / 8 heads x 128, E4M3: 177 us, 5.65 TB/s
+// (0.86 of a copy's rate; the loads alone take 155 us); 32 sequences to 4096, 32 heads,
+// INT4: 113 us, bound by about 400 instructions per tile at half the bytes; two
+// tiles at a time per warp: the same.  1 sequence at 1000 tokens: 8 us, and 4 for
+// the join.
 
 #include <cuda_fp16.h>
 #include <math.h>
