@@ -1,6 +1,6 @@
 // w4kv_attn_rows.cu -- attention of few rows over the quantized cache: decode
-// steps and short proposals, up to 16 (row, query head) pairs per key/value
-// head.
+// steps and short proposals, up to 64 (row, query head) pairs per key/value
+// head, in tiles of 8 or 16.
 //
 // Mathematics: one pass over the cache with a running maximum m, sum l and
 // output O per row; a score is q . codes times the key row's scale, a weight
@@ -8,8 +8,8 @@
 // exactly: INT8 and E4M3 are fp16 numbers, and so are u - z and 16 (u - z) of
 // INT4, which saves half of the shifts.  (The fp16 subnormals u * 2^-24, with the
 // zero points taken off the sums, would save the subtraction, but the MMA aligns
-// them as if they were 2^-14: errors of 2^-14 of the largest product.)  m moves only when a score exceeds it by
-// 2^8, so that O is rarely rescaled; p <= 2^8 then, and the value scales are
+// them as if they were 2^-14: errors of 2^-14 of the largest product.)  m moves
+// only when a score exceeds it by 8 (2^8 in the weights), so that O is rarely rescaled; p <= 2^8 then, and the value scales are
 // taken relative to 2^k > their running maximum / 2^7, so that a weight fits
 // fp16 (below 2^15) with 21 bits of range under the largest one.
 //
@@ -41,8 +41,6 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
-#include <type_traits>
-
 #include "w4kv_attn.cuh"
 
 namespace w4 {
@@ -58,7 +56,6 @@ struct Shape {
     static constexpr int kKB = kRow / 4, kVB = kRow / 8;       // a lane's bytes of a key / value row
     static constexpr int kStage = 2 * kTile * kRow + 128;      // codes, then 32 scale words
     static constexpr int kBlocks = rows_blocks_per_sm(8 * NT);
-    static constexpr int kAtOnce = 1;                // tiles that a warp takes at a time
     static constexpr int kStages = kRow == 128 ? (NT == 1 ? 3 : 5) : (NT == 1 ? 5 : 8);
     static constexpr int kSteps = D / 16;  // k steps of S, row tiles of O^T
     static constexpr int kTileRows = 8 * NT;
@@ -378,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
         }
         int vexp = 7;  // exponent field of the largest value scale so far (at least 7): weights are p * scale * 2^(133 - vexp)
 
-        auto consume = [&](auto np_tag) {
-            constexpr int NP = decltype(np_tag)::value;
+        auto consume = [&]() {
+            constexpr int NP = 1;  // tiles at a time (2: the same speed, more registers)
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - NP) : "memory");
             __syncwarp();
             uint32_t kw[NP][2][S::kKB / 4], ksw[NP][2], vsw[NP][2];
@@ -642,9 +639,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
             get = get + NP < S::kStages ? get + NP : get + NP - S::kStages;
             w.next += NP * kWarps;
         };
-        if (S::kAtOnce == 2)
-            while (w.next + kWarps < w.end) consume(std::integral_constant<int, 2>());
-        while (w.next < w.end) consume(std::integral_constant<int, 1>());
+        while (w.next < w.end) consume();
 
         // ---- the warps' results together ----
 #pragma unroll
