@@ -34,7 +34,7 @@
 //
 // Measured: 64 sequences to 16384 tokens, 64 / 8 heads x 128, E4M3: 177 us, 5.65 TB/s
 // (0.86 of a copy's rate; the loads alone take 155 us); 32 sequences to 4096, 32 heads,
-// INT4: 113 us, bound by about 400 instructions per tile at half the bytes; two
+// INT4: 111 us, bound by about 400 instructions per tile at half the bytes; two
 // tiles at a time per warp: the same.  1 sequence at 1000 tokens: 8 us, and 4 for
 // the join.
 
