@@ -157,6 +157,16 @@ __device__ __forceinline__ int stream_steps(const Attn &a, const Walk &w, int t)
     return min(ns, max(0, (hi - w.lo + kStep - 1) / kStep - w.u0));
 }
 
+// Steps of the current segment for which stream t has MMAs of its own.  A
+// segment without any (a row tile that sees nothing, or none of the block's
+// part) passes none of the stream's barriers, q_full among them: every phase of
+// q_full is then followed by an s_full that the softmax waits for, so that it
+// cannot complete a second phase before the MMA warp has seen the first (a
+// one-bit parity would not show two).
+__device__ __forceinline__ int own_steps(const Attn &a, const Walk &w, int t) {
+    return w.R <= kM ? (w.u1 - w.u0 + 1 - t) >> 1 : stream_steps(a, w, t);
+}
+
 // The warp's walk in shared memory, moved by lane 0.
 __device__ __forceinline__ bool warp_next(const Attn &a, Walk *w) {
     __syncwarp();
@@ -495,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             // ---- the query row: scaled by a power of two, fp16, swizzled ----
             // D / 8 lanes read a row together; lane i keeps the factor of row i of the warp.
             float fr = 1.f;
-            {
+            if (own_steps(a, w, t) > 0) {
                 constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;
                 const int part = lane % kLanes, sub = lane / kLanes;
                 uint8_t *qs = base + L::kQ + t * L::kTile + (part >> 3) * L::kBlock;
@@ -955,16 +965,16 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         const uint32_t k0 = desc_low(smem_u32(base + L::kKV), 16);
         const uint32_t v0 = desc_low(smem_u32(base + L::kKV), L::kBlock);
         const uint32_t d_s = tS + t * kStep, d_o = tO + t * 128;
-        uint32_t step0 = 0, seg_no = 0, n_p = 0;
+        uint32_t step0 = 0, n_q = 0, n_p = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             ok = __all_sync(0xffffffffu, ok && bar_wait(smem_u32(bar), parity, abort_flag, a.status));
             return ok;
         };
-        for (; more && ok; more = warp_next(a, &w), ++seg_no) {
+        for (; more && ok; more = warp_next(a, &w)) {
             const bool split = w.R <= kM;
             const int ns = w.u1 - w.u0, mine = stream_steps(a, w, t);
-            if (!wait(&sm->q_full[t], seg_no & 1)) break;
+            if (own_steps(a, w, t) > 0 && !wait(&sm->q_full[t], n_q++ & 1)) break;
             auto filled = [&](uint32_t n) { return wait(&sm->full[n % kBuffers], (n / kBuffers) & 1); };
             auto let_go = [&](uint32_t n) {
                 if (lane == 0) mbar_arrive(smem_u32(&sm->empty[n % kBuffers]));
