@@ -34,8 +34,8 @@
 //
 // Measured: 64 sequences to 16384 tokens, 64 / 8 heads x 128, E4M3: 177 us, 5.65 TB/s
 // (0.86 of a copy's rate; the loads alone take 155 us); 32 sequences to 4096, 32 heads,
-// INT4: 111 us, bound by about 400 instructions per tile at half the bytes; two
-// tiles at a time per warp: the same.  1 sequence at 1000 tokens: 8 us, and 4 for
+// INT4: 111 us, bound by about 400 instructions per tile at half the bytes (two
+// tiles at a time per warp took the same time).  1 sequence at 1000 tokens: 8 us, and 4 for
 // the join.
 
 #include <cuda_fp16.h>
@@ -376,117 +376,99 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
         int vexp = 7;  // exponent field of the largest value scale so far (at least 7): weights are p * scale * 2^(133 - vexp)
 
         auto consume = [&]() {
-            constexpr int NP = 1;  // tiles at a time (2: the same speed, more registers)
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - NP) : "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
             __syncwarp();
-            uint32_t kw[NP][2][S::kKB / 4], ksw[NP][2], vsw[NP][2];
-            bool bad[NP];
+            uint32_t kw[2][S::kKB / 4], ksw[2], vsw[2];
+            const uint8_t *st = ring + get * S::kStage;
+            const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + 2 * kTile * S::kRow);
+            const bool bad = (bad_mask >> get) & 1;
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                const int slot = get + n < S::kStages ? get + n : get + n - S::kStages;
-                const uint8_t *st = ring + slot * S::kStage;
-                bad[n] = (bad_mask >> slot) & 1;
+            for (int i = 0; i < 2; ++i) {  // rows g, g + 8: the same piece offsets, 8 rows on
+                if (S::kKB >= 16) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {  // rows g, g + 8: the same piece offsets, 8 rows on
-                    if (S::kKB >= 16) {
-#pragma unroll
-                        for (int j = 0; j < S::kKB / 16; ++j) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(
-                                st + piece_at<S::kRow>(g, c * (S::kKB / 16) + j) + i * 8 * S::kRow);
-                            kw[n][i][4 * j] = v.x, kw[n][i][4 * j + 1] = v.y;
-                            kw[n][i][4 * j + 2] = v.z, kw[n][i][4 * j + 3] = v.w;
-                        }
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(
-                            st + piece_at<S::kRow>(g, c >> 1) + (c & 1) * 8 + i * 8 * S::kRow);
-                        kw[n][i][0] = v.x, kw[n][i][1] = v.y;
+                    for (int j = 0; j < S::kKB / 16; ++j) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            st + piece_at<S::kRow>(g, c * (S::kKB / 16) + j) + i * 8 * S::kRow);
+                        kw[i][4 * j] = v.x, kw[i][4 * j + 1] = v.y;
+                        kw[i][4 * j + 2] = v.z, kw[i][4 * j + 3] = v.w;
                     }
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(
+                        st + piece_at<S::kRow>(g, c >> 1) + (c & 1) * 8 + i * 8 * S::kRow);
+                    kw[i][0] = v.x, kw[i][1] = v.y;
                 }
-                const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + 2 * kTile * S::kRow);
-                ksw[n][0] = sw[g], ksw[n][1] = sw[g + 8];
-                vsw[n][0] = sw[16 + g], vsw[n][1] = sw[24 + g];
             }
+            ksw[0] = sw[g], ksw[1] = sw[g + 8];
+            vsw[0] = sw[16 + g], vsw[1] = sw[24 + g];
             // ---- S^T = K Q^T ----
-            float sc[NP][NT][4];
+            float sc[NT][4];
 #pragma unroll
-            for (int n = 0; n < NP; ++n)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < 4; ++i) sc[nt][i] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[n][nt][i] = 0.f;
+            for (int s = 0; s < S::kSteps; ++s) {
+                uint32_t fa[4];
+                if (FMT == W4KV_INT4) {
 #pragma unroll
-            for (int s = 0; s < S::kSteps; ++s)
-#pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    uint32_t fa[4];
-                    if (FMT == W4KV_INT4) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {  // u - z, then 16 (u - z), of rows g, g + 8
-                            const uint32_t x = kw[n][q & 1][s >> 1] >> (8 * (s & 1));
-                            const uint32_t u = (x & (q & 2 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
-                            const uint32_t z = (ksw[n][q & 1] & 15u) * (q & 2 ? 0x100010u : 0x10001u) | 0x64006400u;
-                            const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u),
-                                                      *reinterpret_cast<const __half2 *>(&z));
-                            fa[q] = *reinterpret_cast<const uint32_t *>(&r);
-                        }
-                    } else {
-                        widen4<FMT>(kw[n][0][s], &fa[0], &fa[2]);
-                        widen4<FMT>(kw[n][1][s], &fa[1], &fa[3]);
+                    for (int q = 0; q < 4; ++q) {  // u - z, then 16 (u - z), of rows g, g + 8
+                        const uint32_t x = kw[q & 1][s >> 1] >> (8 * (s & 1));
+                        const uint32_t u = (x & (q & 2 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+                        const uint32_t z = (ksw[q & 1] & 15u) * (q & 2 ? 0x100010u : 0x10001u) | 0x64006400u;
+                        const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u),
+                                                  *reinterpret_cast<const __half2 *>(&z));
+                        fa[q] = *reinterpret_cast<const uint32_t *>(&r);
                     }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma(sc[n][nt], fa, bq[nt][s][0], bq[nt][s][1]);
+                } else {
+                    widen4<FMT>(kw[0][s], &fa[0], &fa[2]);
+                    widen4<FMT>(kw[1][s], &fa[1], &fa[3]);
                 }
-            // ---- scores in base 2, masked ----
-            bool grow = false, any_cut = false;
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                const int kv0 = (w.next + n * kWarps) * kTile;
-                const bool cut = bad[n] || kv0 < all_lo || kv0 + kTile > all_hi;  // warp-uniform
-                any_cut = any_cut || cut;
+                for (int nt = 0; nt < NT; ++nt) mma(sc[nt], fa, bq[nt][s][0], bq[nt][s][1]);
+            }
+            // ---- scores in base 2, masked ----
+            bool grow = false;
+            const int kv0 = w.next * kTile;
+            const bool cut = bad || kv0 < all_lo || kv0 + kTile > all_hi;  // warp-uniform
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = i & 1;
+                    const uint32_t kw_ = ksw[i >> 1];
+                    float x = sc[nt][i];
+                    x *= FMT == W4KV_INT4 ? int4_scale(kw_) : __uint_as_float(kw_);
+                    sc[nt][i] = x * f[nt][e];
+                }
+            if (cut) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int e = i & 1;
-                        const uint32_t kw_ = ksw[n][i >> 1];
-                        float x = sc[n][nt][i];
-                        x *= FMT == W4KV_INT4 ? int4_scale(kw_) : __uint_as_float(kw_);
-                        sc[n][nt][i] = x * f[nt][e];
+                        const int j = kv0 + g + 8 * (i >> 1), pos = qpos[nt][i & 1];
+                        if (bad || j < w.lo || j >= w.hi || (a.causal && j > pos) ||
+                            (a.window > 0 && j <= pos - a.window))
+                            sc[nt][i] = -INFINITY;
                     }
-                if (cut) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int j = kv0 + g + 8 * (i >> 1), pos = qpos[nt][i & 1];
-                            if (bad[n] || j < w.lo || j >= w.hi || (a.causal && j > pos) ||
-                                (a.window > 0 && j <= pos - a.window))
-                                sc[n][nt][i] = -INFINITY;
-                        }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) grow = grow || sc[n][nt][i] > m[nt][i & 1] + 8.f;
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) grow = grow || sc[nt][i] > m[nt][i & 1] + 8.f;
             // ---- new reference maxima and value exponent, if they moved ----
-            if (any_cut) {  // scales of rows out of use may be anything
+            if (cut) {  // scales of rows out of use may be anything
 #pragma unroll
-                for (int n = 0; n < NP; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int j = (w.next + n * kWarps) * kTile + g + 8 * i;
-                        if (bad[n] || j < w.lo || j >= w.hi) vsw[n][i] = 0;
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    const int j = kv0 + g + 8 * i;
+                    if (bad || j < w.lo || j >= w.hi) vsw[i] = 0;
+                }
             }
             uint32_t ve = 0;
 #pragma unroll
-            for (int n = 0; n < NP; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t e = (vsw[n][i] >> 23) & 255u;
-                    ve = max(ve, e == 255u ? 0u : e);
-                }
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t e = (vsw[i] >> 23) & 255u;
+                ve = max(ve, e == 255u ? 0u : e);
+            }
             ve = __reduce_max_sync(0xffffffffu, ve);
             const bool vgrow = static_cast<int>(ve) > vexp;
             if (__any_sync(0xffffffffu, grow) || vgrow) {
@@ -501,8 +483,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float x = m[nt][e];
-#pragma unroll
-                        for (int n = 0; n < NP; ++n) x = fmaxf(x, fmaxf(sc[n][nt][e], sc[n][nt][e + 2]));
+                        x = fmaxf(x, fmaxf(sc[nt][e], sc[nt][e + 2]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
                         fo[e] = ex2(m[nt][e] - x);
@@ -521,123 +502,111 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
             // For fp16 outputs a weight is fed as the sum of two fp16 numbers: one alone would
             // err as much as the output's own rounding (0.0003 instead of 0.0002 in all).
             constexpr int kParts = XT == W4_F16 ? 2 : 1;
-            uint32_t pb[kParts][NP][NT][2];
+            uint32_t pb[kParts][NT][2];
 #pragma unroll
-            for (int n = 0; n < NP; ++n)
+            for (int i = 0; i < 2; ++i) {  // tokens g, g + 8
+                const uint32_t vw_ = vsw[i];
+                const float vs = (FMT == W4KV_INT4 ? int4_scale(vw_) : __uint_as_float(vw_)) * vmul;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {  // tokens g, g + 8
-                    const uint32_t vw_ = vsw[n][i];
-                    const float vs = (FMT == W4KV_INT4 ? int4_scale(vw_) : __uint_as_float(vw_)) * vmul;
+                for (int nt = 0; nt < NT; ++nt) {
+                    float pw[2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float pw[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = sc[n][nt][2 * i + e];
-                            const float pe = ex2(x - m[nt][e]);
-                            l[nt][e] += pe;
-                            pw[e] = pe * vs;
-                            // unseen: exactly zero, whatever the value row's scale is
-                            if (any_cut && x == -INFINITY) pw[e] = 0.f;
-                        }
-                        __half2 h = __floats2half2_rn(pw[0], pw[1]);
-                        pb[0][n][nt][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
-                        if (kParts == 2) {
-                            const float2 r = __half22float2(h);
-                            h = __floats2half2_rn(pw[0] - r.x, pw[1] - r.y);
-                            pb[kParts - 1][n][nt][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = sc[nt][2 * i + e];
+                        const float pe = ex2(x - m[nt][e]);
+                        l[nt][e] += pe;
+                        pw[e] = pe * vs;
+                        // unseen: exactly zero, whatever the value row's scale is
+                        if (cut && x == -INFINITY) pw[e] = 0.f;
+                    }
+                    __half2 h = __floats2half2_rn(pw[0], pw[1]);
+                    pb[0][nt][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
+                    if (kParts == 2) {
+                        const float2 r = __half22float2(h);
+                        h = __floats2half2_rn(pw[0] - r.x, pw[1] - r.y);
+                        pb[kParts - 1][nt][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
                     }
                 }
+            }
             // ---- O^T += V^T P^T ----
-            uint32_t vw[NP][4][S::kVB / 4];
-            uint32_t vz[NP][2];  // zero points of the value rows 2c, 2c + 1 and 2c + 8, 2c + 9
+            uint32_t vw[4][S::kVB / 4];
+            uint32_t vz[2];  // zero points of the value rows 2c, 2c + 1 and 2c + 8, 2c + 9
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                const int slot = get + n < S::kStages ? get + n : get + n - S::kStages;
-                const uint8_t *st = ring + slot * S::kStage;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t *vp = st + kTile * S::kRow + (i >> 1) * 8 * S::kRow +
-                                        piece_at<S::kRow>(2 * c + (i & 1), g * S::kVB / 16) +
-                                        (g * S::kVB) % 16;
-                    if (S::kVB == 16) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(vp);
-                        vw[n][i][0] = v.x, vw[n][i][1] = v.y, vw[n][i][2] = v.z, vw[n][i][3] = v.w;
-                    } else if (S::kVB == 8) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(vp);
-                        vw[n][i][0] = v.x, vw[n][i][1] = v.y;
-                    } else {
-                        vw[n][i][0] = *reinterpret_cast<const uint32_t *>(vp);
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *vp = st + kTile * S::kRow + (i >> 1) * 8 * S::kRow +
+                                    piece_at<S::kRow>(2 * c + (i & 1), g * S::kVB / 16) +
+                                    (g * S::kVB) % 16;
+                if (S::kVB == 16) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(vp);
+                    vw[i][0] = v.x, vw[i][1] = v.y, vw[i][2] = v.z, vw[i][3] = v.w;
+                } else if (S::kVB == 8) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(vp);
+                    vw[i][0] = v.x, vw[i][1] = v.y;
+                } else {
+                    vw[i][0] = *reinterpret_cast<const uint32_t *>(vp);
                 }
-                if (FMT == W4KV_INT4) {
-                    const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + 2 * kTile * S::kRow);
+            }
+            if (FMT == W4KV_INT4) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint2 z = *reinterpret_cast<const uint2 *>(sw + 16 + 2 * c + 8 * q);
-                        vz[n][q] = (z.x & 15u) | (z.y & 15u) << 16;
-                    }
+                for (int q = 0; q < 2; ++q) {
+                    const uint2 z = *reinterpret_cast<const uint2 *>(sw + 16 + 2 * c + 8 * q);
+                    vz[q] = (z.x & 15u) | (z.y & 15u) << 16;
                 }
             }
             __syncwarp();
+            issue();
+            if (FMT == W4KV_INT4) {
 #pragma unroll
-            for (int n = 0; n < NP; ++n) issue();
+                for (int j = 0; j < S::kVB / 4; ++j) {
+                    uint32_t x[2][2];  // [low, high nibbles' halves][tokens 2c.., 2c + 8..]
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                if (FMT == W4KV_INT4) {
-#pragma unroll
-                    for (int j = 0; j < S::kVB / 4; ++j) {
-                        uint32_t x[2][2];  // [low, high nibbles' halves][tokens 2c.., 2c + 8..]
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            x[0][q] = prmt(vw[n][2 * q][j], vw[n][2 * q + 1][j], 0x5410);
-                            x[1][q] = prmt(vw[n][2 * q][j], vw[n][2 * q + 1][j], 0x7632);
-                        }
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {  // dims 8j + 2t, 8j + 2t + 1; 16-fold for odd t
-                            // 1024 + u as fp16 bits 0x6400 | u (or 16 u), then - (1024 + z)
-                            const uint32_t mask = t & 1 ? 0x00F000F0u : 0x000F000Fu;
-                            const int sh = t & 2 ? 8 : 0;
-                            uint32_t fa[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const uint32_t u = ((x[q & 1][q >> 1] >> sh) & mask) | 0x64006400u;
-                                const uint32_t z = (vz[n][q >> 1] << (t & 1 ? 4 : 0)) | 0x64006400u;
-                                const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u),
-                                                          *reinterpret_cast<const __half2 *>(&z));
-                                fa[q] = *reinterpret_cast<const uint32_t *>(&r);
-                            }
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int q = 0; q < kParts; ++q)
-                                    mma(o[nt][4 * j + t], fa, pb[q][n][nt][0], pb[q][n][nt][1]);
-                        }
+                    for (int q = 0; q < 2; ++q) {
+                        x[0][q] = prmt(vw[2 * q][j], vw[2 * q + 1][j], 0x5410);
+                        x[1][q] = prmt(vw[2 * q][j], vw[2 * q + 1][j], 0x7632);
                     }
-                } else {
 #pragma unroll
-                    for (int j = 0; j < S::kVB / 4; ++j) {
-                        uint32_t fa[2][4];  // dims 4j, 4j + 1 and 4j + 2, 4j + 3
+                    for (int t = 0; t < 4; ++t) {  // dims 8j + 2t, 8j + 2t + 1; 16-fold for odd t
+                        // 1024 + u as fp16 bits 0x6400 | u (or 16 u), then - (1024 + z)
+                        const uint32_t mask = t & 1 ? 0x00F000F0u : 0x000F000Fu;
+                        const int sh = t & 2 ? 8 : 0;
+                        uint32_t fa[4];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const uint32_t x = prmt(vw[n][2 * q][j], vw[n][2 * q + 1][j], 0x5140);
-                            const uint32_t y = prmt(vw[n][2 * q][j], vw[n][2 * q + 1][j], 0x7362);
-                            widen4<FMT>(x, &fa[0][2 * q], &fa[0][2 * q + 1]);
-                            widen4<FMT>(y, &fa[1][2 * q], &fa[1][2 * q + 1]);
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t u = ((x[q & 1][q >> 1] >> sh) & mask) | 0x64006400u;
+                            const uint32_t z = (vz[q >> 1] << (t & 1 ? 4 : 0)) | 0x64006400u;
+                            const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u),
+                                                      *reinterpret_cast<const __half2 *>(&z));
+                            fa[q] = *reinterpret_cast<const uint32_t *>(&r);
                         }
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int q = 0; q < kParts; ++q)
-                                    mma(o[nt][2 * j + t], fa[t], pb[q][n][nt][0], pb[q][n][nt][1]);
+                            for (int q = 0; q < kParts; ++q)
+                                mma(o[nt][4 * j + t], fa, pb[q][nt][0], pb[q][nt][1]);
                     }
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < S::kVB / 4; ++j) {
+                    uint32_t fa[2][4];  // dims 4j, 4j + 1 and 4j + 2, 4j + 3
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t x = prmt(vw[2 * q][j], vw[2 * q + 1][j], 0x5140);
+                        const uint32_t y = prmt(vw[2 * q][j], vw[2 * q + 1][j], 0x7362);
+                        widen4<FMT>(x, &fa[0][2 * q], &fa[0][2 * q + 1]);
+                        widen4<FMT>(y, &fa[1][2 * q], &fa[1][2 * q + 1]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int q = 0; q < kParts; ++q)
+                                mma(o[nt][2 * j + t], fa[t], pb[q][nt][0], pb[q][nt][1]);
+                }
             }
-            get = get + NP < S::kStages ? get + NP : get + NP - S::kStages;
-            w.next += NP * kWarps;
+            get = get + 1 == S::kStages ? 0 : get + 1;
+            w.next += kWarps;
         };
         while (w.next < w.end) consume();
 
