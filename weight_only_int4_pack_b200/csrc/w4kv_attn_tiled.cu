@@ -336,7 +336,24 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) 
                  : "memory");
 }
 
-// Waits for the loads issued so far; r depends on it.
+// Waits for the loads issued so far; r depends on it, so that nothing made of r
+// comes before.
+__device__ __forceinline__ void tmem_wait_ld8(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7])::"memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
 __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
@@ -634,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                             for (int c = 0; c < cols; c += 8) {
                                 uint32_t p[8];
                                 tmem_ld8(s_col + c, p);
-                                tmem_wait_ld();
+                                tmem_wait_ld8(p);
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
                                     const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&p[i]), f2);
@@ -718,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                 weights(y, c, l2, p);
                                 float sum = unpack2(l2).x + unpack2(l2).y;
                                 if (__any_sync(0xffffffffu, sum > 256.f)) {
+                                    if (c < 7) tmem_wait_ld16(s);  // the next scores: not in flight below
                                     float top = 0.f;
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(unpack2(y[i]).x, unpack2(y[i]).y));
@@ -793,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                     uint32_t o[32];
                     if (own > 0) {
                         tmem_ld32(o_col + 32 * c, o);
-                        tmem_wait_ld();
+                        tmem_wait_ld32(o);
                     }
                     float x[32];
 #pragma unroll
@@ -838,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                         uint32_t o[32];
                         if (own > 0) {
                             tmem_ld32(o_col + 32 * c, o);
-                            tmem_wait_ld();
+                            tmem_wait_ld32(o);
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
