@@ -139,11 +139,12 @@ size_t w4kv_attention_workspace_bytes(const w4kv_cache *cache, int64_t batch, in
  *          status word reports W4_ERR_BOUNDS.
  *   Numerics: codes enter the tensor cores unrounded (they are exact in fp16);
  *   scores, maxima, sums and outputs are fp32; the probabilities times the
- *   value scales are rounded to fp16 (relative to a running power of two, so
- *   that no scale leaves the range: what is lost is below 2^-32 of the largest
- *   value); the output is rounded once.  Queries enter as fp16, each row scaled
- *   by a power of two: exact for elements down to 2^-14 of the row's largest,
- *   smaller ones carry an error of at most 2^-25 of it.
+ *   value scales are rounded to fp16 (relative to a running power of two of
+ *   each row, so that no scale leaves the range: a token loses at most 2^-31,
+ *   W4KV_INT4 2^-30, of the largest value that the row sees); the output is
+ *   rounded once.  Queries enter as fp16, each row scaled by a power of two:
+ *   exact for elements down to 2^-14 of the row's largest, smaller ones carry
+ *   an error of at most 2^-25 of it.
  *   Q and what the cache's visible rows stand for must be finite for a finite
  *   result, and keys below 1e34.  Deterministic: repeated calls give the same bits.
  *   Sequences with at most 64 (row, query head) pairs per key/value head run on

@@ -62,3 +62,114 @@ def test_short_items_in_every_block(w4):
         O, lse = w4.w4kv_attention(Q.cuda(), p.device(w4), *p.batch(n_rows), max_rows=257,
                                    causal=causal, return_lse=True)
         close(O, lse, R.attention(p, Q, n_rows, 0.125, causal), str(causal))
+
+
+# ---- what a row does not see has no influence, whatever it holds -------------------------------
+
+def row_tolerance(p, Q, n_rows, scale, causal=True, window=0):
+    """R.attention with the absolute term of the tolerance taken per row, over
+    the tokens that this row sees.  A weight is fed as fp16(prob * s * 2^(133 - e)),
+    e the exponent field of the largest scale that the row sees: below fp16's
+    normal range it is off by at most 2^-25, so the token's part by
+    2^-25 * code * 2^(e - 133) <= 2^-31 * largest code * largest scale; the token
+    of the largest scale has an element of that size (INT8, E4M3) or of half of
+    it (INT4: one of 15 units' ends is 7.5 or more from zero).  The sum of the
+    probabilities that divides it is 1 at least."""
+    O, lse, tol, ltol = R.attention(p, Q, n_rows, scale, causal, window)
+    T, H, D = Q.shape
+    G = H // p.Hk
+    u = torch.finfo(Q.dtype).eps / 2
+    t = 0
+    for b, n in enumerate(n_rows):
+        L = p.lens[b]
+        k, v = (torch.from_numpy(R.values(*p.rows(i, b), p.fmt)) for i in range(2))
+        q = Q[t:t + n].double()
+        pos, col = torch.arange(L - n, L)[:, None], torch.arange(L)[None, :]
+        seen = torch.ones((n, L), dtype=torch.bool)
+        if causal:
+            seen = col <= pos
+            if window:
+                seen &= col > pos - window
+        for h in range(H):
+            s = torch.where(seen, (q[:, h] @ k[:, h // G].T) * scale, -torch.inf)
+            w = torch.softmax(s, -1)
+            va = v[:, h // G].abs()
+            sa = torch.where(seen, (q[:, h].abs() @ k[:, h // G].abs().T) * abs(scale), torch.zeros_like(s))
+            smax = sa.amax(-1)
+            d = 2 * (smax * (D + 8) * 2.0 ** -23 + 2.0 ** -22 + 2.0 ** -23 * smax * 1.4427) + (L + 8) * 2.0 ** -23
+            vmax = torch.where(seen, va.amax(-1)[None, :], 0).amax(-1)
+            lost = seen.sum(-1) * 2.0 ** (-30 if p.fmt == R.INT4 else -31) * vmax
+            tol[t:t + n, h] = u * O[t:t + n, h].abs() + (1 + u) * (w @ va) * (2.0 ** -11 + d[:, None]) + lost[:, None]
+        t += n
+    return O, lse, tol, ltol
+
+
+# (rows, query heads of two key/value heads): the row kernel's tiles of 8 and 16, several of
+# those, one split row tile, two row tiles, several items
+SHAPES = [(3, 2), (6, 4), (20, 4), (40, 4), (100, 4), (300, 4)]
+COPIES = (1, 50)
+UNSEEN = [(399, 0), (398, 0), (10, 64), (250, 100)]  # position of a token, window
+
+
+def shared(p, n, copies):
+    """The batch of `copies` sequences in the pages of one, so that a block walks several steps."""
+    return (torch.from_numpy(p.table.repeat(copies, 0)).cuda(),
+            torch.full((copies,), p.lens[0], dtype=torch.int32, device="cuda"),
+            torch.arange(copies + 1, dtype=torch.int32, device="cuda") * n)
+
+
+def close_copies(O, lse, want, copies):
+    n = O.shape[0] // copies
+    for i in range(copies):
+        close(O[i * n:(i + 1) * n], lse[i * n:(i + 1) * n], want, f"copy {i}")
+
+
+def token_rows(L, n, at, window):
+    pos = torch.arange(L - n, L)
+    return (pos >= at) & (pos - (window or L + 1) < at)
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("n,H", SHAPES)
+@pytest.mark.parametrize("copies", COPIES)
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_unseen_sizes(w4, fmt, copies, n, H, dtype):
+    """A token with a key or a value of 1e30 leaves the rows that do not see it
+    as they were, bit for bit."""
+    L, D = 400, 64
+    p = R.Plain([L], fmt, 2, D, 16, 1)
+    Q = rows((n * copies, H, D), dtype, 2).cuda()
+    batch = shared(p, n, copies)
+    r = np.random.default_rng(5)
+    for at, window in UNSEEN:
+        want = w4.w4kv_attention(Q, p.device(w4), *batch, max_rows=n, window=window)
+        sees = token_rows(L, n, at, window).cuda().repeat(copies)
+        pg, off = (int(x) for x in p.at(0, at))
+        for which in range(2):
+            bad = p.device(w4)
+            code, word = R.quantize((r.standard_normal((1, D)) * 1e30).astype(np.float32), fmt)
+            c, s = ((bad.k_codes, bad.k_scales), (bad.v_codes, bad.v_scales))[which]
+            c[pg, 0, off] = torch.from_numpy(code[0]).cuda()
+            s[pg, 0, off] = float(word.view(np.float32)[0])
+            got = w4.w4kv_attention(Q, bad, *batch, max_rows=n, window=window)
+            assert torch.equal(got[:, H // 2:], want[:, H // 2:])
+            assert torch.equal(got[~sees], want[~sees]), (at, window, which)
+
+
+@pytest.mark.parametrize("copies", COPIES)
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("n,H", SHAPES)
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_value_sizes_per_row(w4, fmt, n, H, window, copies):
+    """Values from 1e-12 to 1e12, growing along the sequence and at random:
+    each row within the tolerance of what it sees itself."""
+    L, D = 400, 64
+    r = np.random.default_rng(3)
+    for sizes in (np.linspace(-12, 12, L), np.linspace(12, -12, L), r.uniform(-12, 12, L)):
+        p = R.Plain([L], fmt, 2, D, 16, 1, dtype=torch.bfloat16)
+        v = r.standard_normal((L, 2, D)) * 10.0 ** sizes[:, None, None]
+        p.store(1, 0, 0, *R.quantize(v.astype(np.float32), fmt))
+        Q = rows((n, H, D), torch.bfloat16, 2)
+        O, lse = w4.w4kv_attention(Q.cuda().repeat(copies, 1, 1), p.device(w4), *shared(p, n, copies),
+                                   max_rows=n, window=window, return_lse=True)
+        close_copies(O, lse, row_tolerance(p, Q, [n], D ** -0.5, True, window), copies)

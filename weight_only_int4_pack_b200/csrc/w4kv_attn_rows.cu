@@ -10,8 +10,8 @@
 // zero points taken off the sums, would save the subtraction, but the MMA aligns
 // them as if they were 2^-14: errors of 2^-14 of the largest product.)  m moves
 // only when a score exceeds it by 8 (2^8 in the weights), so that O is rarely rescaled; p <= 2^8 then, and the value scales are
-// taken relative to 2^k > their running maximum / 2^7, so that a weight fits
-// fp16 (below 2^15) with 21 bits of range under the largest one.
+// taken relative to 2^k > the running maximum / 2^7 of those that the row sees, so
+// that a weight fits fp16 (below 2^15) with 21 bits of range under the largest one.
 //
 // HBM bounds it: a token of a head is 2 (dim + 4) bytes (INT8) and a few
 // thousand multiplications.  The layout keeps the shared-memory and register
@@ -373,7 +373,14 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[nt][t][i] = 0.f;
         }
-        int vexp = 7;  // exponent field of the largest value scale so far (at least 7): weights are p * scale * 2^(133 - vexp)
+        // A weight is fed as p * scale * vref, vref = 2^(133 - e) with e the exponent field of the
+        // largest value scale that the column's row has seen (at least 7).  Each column has its
+        // own: one for the tile would let tokens that a row does not see shift its weights out of
+        // fp16's range.  For the same reason a column's maximum moves only by its own scores
+        // where other columns' may be of tokens that it does not see.
+        float vref[NT][2], vmax = pow2i(126);  // vmax: the lane's largest
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) vref[nt][0] = vref[nt][1] = vmax;
 
         auto consume = [&]() {
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
@@ -463,33 +470,41 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                     if (bad || j < w.lo || j >= w.hi) vsw[i] = 0;
                 }
             }
-            uint32_t ve = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t e = (vsw[i] >> 23) & 255u;
-                ve = max(ve, e == 255u ? 0u : e);
-            }
-            ve = __reduce_max_sync(0xffffffffu, ve);
-            const bool vgrow = static_cast<int>(ve) > vexp;
-            if (__any_sync(0xffffffffu, grow) || vgrow) {
-                float fv = 1.f;
-                if (vgrow) {
-                    fv = pow2i(max(-126, vexp - static_cast<int>(ve)));
-                    vexp = static_cast<int>(ve);
-                }
+            auto exponent = [](uint32_t scale) {  // its field; none for infinities and NaN
+                const uint32_t e = (scale >> 23) & 255u;
+                return e == 255u ? 0u : e;
+            };
+            const uint32_t ve = __reduce_max_sync(0xffffffffu, max(max(exponent(vsw[0]), exponent(vsw[1])), 7u));
+            const float vtile = pow2i(133 - static_cast<int>(ve));
+            if (__any_sync(0xffffffffu, grow || vtile < vmax)) {
+                // (without a window, cut tiles are an item's last)
+                const bool own_moves = cut || a.window > 0;
+                vmax = 0.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float fo[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = m[nt][e];
-                        x = fmaxf(x, fmaxf(sc[nt][e], sc[nt][e + 2]));
+                        float x = fmaxf(sc[nt][e], sc[nt][e + 2]), v = vtile;
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        x = !own_moves || x > m[nt][e] + 8.f ? fmaxf(x, m[nt][e]) : m[nt][e];
+                        if (cut) {  // of the tokens that the row sees
+                            uint32_t t = 7;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (sc[nt][2 * i + e] != -INFINITY) t = max(t, exponent(vsw[i]));
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, d));
+                            v = pow2i(133 - static_cast<int>(t));
+                        }
+                        v = fminf(v, vref[nt][e]);
                         fo[e] = ex2(m[nt][e] - x);
                         m[nt][e] = x;
                         l[nt][e] *= fo[e];
-                        fo[e] *= fv;
+                        fo[e] *= pow2i(max(-126, static_cast<int>(__float_as_uint(v) - __float_as_uint(vref[nt][e])) >> 23));
+                        vref[nt][e] = v;
+                        vmax = fmaxf(vmax, v);
                     }
 #pragma unroll
                     for (int t = 0; t < S::kSteps; ++t)
@@ -497,7 +512,6 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                         for (int i = 0; i < 4; ++i) o[nt][t][i] *= fo[i & 1];
                 }
             }
-            const float vmul = pow2i(133 - vexp);
             // ---- weights, transposed into B fragments ----
             // For fp16 outputs a weight is fed as the sum of two fp16 numbers: one alone would
             // err as much as the output's own rounding (0.0003 instead of 0.0002 in all).
@@ -505,8 +519,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
             uint32_t pb[kParts][NT][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // tokens g, g + 8
-                const uint32_t vw_ = vsw[i];
-                const float vs = (FMT == W4KV_INT4 ? int4_scale(vw_) : __uint_as_float(vw_)) * vmul;
+                const float vs = FMT == W4KV_INT4 ? int4_scale(vsw[i]) : __uint_as_float(vsw[i]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float pw[2];
@@ -515,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                         const float x = sc[nt][2 * i + e];
                         const float pe = ex2(x - m[nt][e]);
                         l[nt][e] += pe;
-                        pw[e] = pe * vs;
+                        pw[e] = pe * (vs * vref[nt][e]);
                         // unseen: exactly zero, whatever the value row's scale is
                         if (cut && x == -INFINITY) pw[e] = 0.f;
                     }
@@ -626,7 +639,6 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 }
             }
         __syncthreads();
-        const float vback = pow2i(vexp - 133);  // 1 / vmul
         float wgt[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -640,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 for (int q = 0; q < kWarps; ++q)
                     L += stat_l[q * S::kTileRows + r] * ex2(stat_m[q * S::kTileRows + r] - M);
                 wgt[nt][e] = L == 0.f ? 0.f : ex2(m[nt][e] - M) / L;
+                vref[nt][e] = __uint_as_float((254u << 23) - __float_as_uint(vref[nt][e]));  // 1 / vref
             }
         // where the item's units lie among the blocks
         const bool from_start = w.u0 == 0;
@@ -684,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                         }
                         *reinterpret_cast<float2 *>(
                             join + (warp * S::kTileRows + nt * 8 + 2 * c + e) * S::kPad + t * 16 + 2 * g) =
-                            make_float2(x * wgt[nt][e] * vback, y * wgt[nt][e] * vback);
+                            make_float2(x * wgt[nt][e] * vref[nt][e], y * wgt[nt][e] * vref[nt][e]);
                     }
             __syncthreads();
             for (int i = threadIdx.x; i < S::kTileRows * S::kPhase / 2; i += kThreads) {

@@ -5,7 +5,7 @@
 // pairs: two tiles A and B of 128 rows, that share every dequantized key and
 // value tile of 128 cached tokens (a step).  Mathematics as in
 // w4kv_attn_rows.cu (running maximum that moves by 2^8 at least, weights held
-// relative to the largest value scale), with
+// relative to the largest value scale that the row has seen), with
 //     S = Q K^T       tcgen05.mma, both operands in shared memory, fp32 in TMEM
 //     O += P V        tcgen05.mma, P (fp16) read from TMEM, V in shared memory
 // Codes are widened exactly to fp16 (INT4 as u - z); the scales are applied to
@@ -177,13 +177,22 @@ __device__ __forceinline__ bool warp_next(const Attn &a, Walk *w) {
     return more != 0;
 }
 
+// Of a step: the tokens that all rows of the item see, from bits kFrom to kTo; whether it opens a
+// segment.
+constexpr int kFrom = 8, kTo = 16;
+constexpr uint32_t kOpens = 1u << 31;
+
 struct alignas(16) Control {
     float ks[kScaleStages][kStep];  // key scales times scale * log2(e)
-    float vs[kScaleStages][kStep];  // value scales times 2^(133 - vexp)
+    float vs[kScaleStages][kStep];  // value scales times 2^(133 - vexp), or as they are
     uint32_t word[kScaleAhead + 1][2][kStep];  // scale words on their way: keys, values
-    uint32_t word_bad[kScaleAhead + 1];        // their bad groups; bit 31: opens a segment
+    uint32_t word_info[kScaleAhead + 1];       // their bad groups; kFrom, kTo; kOpens
     float stat[2][2][kM];           // [stream][maximum, sum][row], to join split streams
-    int vexp[kScaleStages];         // exponent field the value scales are relative to
+    int row_vexp[2][kM];            // [stream][row]: the row's own vexp, while a warp's rows differ
+    // Largest exponent field (at least 7) of the value scales of the segment's tokens so far that
+    // all rows of the item see; -1 if the step has larger ones, that not all see.
+    int vexp[kScaleStages];
+    uint8_t vgroup[kScaleStages][8];  // then: the largest of each 16 tokens
     uint32_t bad[kScaleStages];     // bit i: tokens 16 i .. 16 i + 15 have no page
     uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
     uint64_t full[kBuffers], empty[kBuffers];
@@ -581,6 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             const bool any_live = __any_sync(0xffffffffu, live);
 
             float m = kNone, l = 0.f;
+            // Weights are p * scale * 2^(133 - e), e the exponent field of the largest value scale
+            // that the row has seen (at least 7): vcur, or row_vexp where that is -1.
             int vcur = 7, own = 0;
             const int ns = w.u1 - w.u0, mine = stream_steps(a, w, t), kv_base = w.lo + w.u0 * kStep;
             for (int j = 0; j < ns && ok; ++j, ++step_no) {
@@ -603,21 +614,29 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                         };
                         const ulonglong2 *ks2 = reinterpret_cast<const ulonglong2 *>(sm->ks[sc]);
                         const ulonglong2 *vs2 = reinterpret_cast<const ulonglong2 *>(sm->vs[sc]);
-                        // 16 scores in units of the row's power of two
-                        auto scores = [&](const uint32_t (&s)[16], int c, uint64_t (&x)[8]) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const ulonglong2 k = ks2[4 * c + i];
-                                x[2 * i] = mul2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k.x);
-                                x[2 * i + 1] = mul2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k.y);
-                            }
-                        };
                         const uint64_t fr2 = pack2(fr, fr);
-                        // Eight pairs of scores over m -> weights; the unscaled ones' sum to l2.
-                        auto weights = [&](const uint64_t (&y)[8], int c, uint64_t &l2, uint32_t (&p)[8]) {
+                        // Eight pairs of scores over m, of the chunk being loaded; then `next`.
+                        auto bases = [&](uint32_t (&s)[16], int c, uint64_t (&y)[8], auto next) {
+                            ulonglong2 k[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) k[i] = ks2[4 * c + i];
+                            const uint64_t m2 = pack2(-m, -m);
+                            tmem_wait_ld16(s);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const ulonglong2 v = vs2[4 * c + i];
+                                y[2 * i] = fma2(mul2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k[i].x), fr2, m2);
+                                y[2 * i + 1] = fma2(mul2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k[i].y), fr2, m2);
+                            }
+                            next();
+                        };
+                        // Eight pairs of scores over m -> weights; the unscaled ones' sum to l2.
+                        // g: the row's reference over the step's, where they may differ.
+                        auto weights = [&](const uint64_t (&y)[8], int c, uint64_t &l2, uint32_t (&p)[8], auto g) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                ulonglong2 v = vs2[4 * c + i];
+                                if constexpr (std::is_same_v<decltype(g), float>)
+                                    v.x = mul2(v.x, pack2(g, g)), v.y = mul2(v.y, pack2(g, g));
                                 const float2 y0 = unpack2(y[2 * i]), y1 = unpack2(y[2 * i + 1]);
                                 const uint64_t p0 = pack2(ex2(y0.x), ex2(y0.y)), p1 = pack2(ex2(y1.x), ex2(y1.y));
                                 l2 = add2(l2, p0);
@@ -662,11 +681,36 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                             tmem_wait_st();
                             return true;
                         };
+                        // The value scales' reference moves with the step's, or where that is none with
+                        // what each row sees.  (One reference for all rows would let tokens that a
+                        // row does not see shift its weights out of fp16's range.)
                         const int ve = sm->vexp[sc];
-                        if (ve != vcur) {  // the value scales' reference moved
-                            ok = rescale(pow2i(max(-126, vcur - ve)), 0);
-                            if (!ok) break;
-                            vcur = ve;
+                        bool own_ref = false;  // rows' references differ from the step's
+                        if (ve != vcur || ve < 0) {
+                            const int old = vcur < 0 ? sm->row_vexp[t][row] : vcur;
+                            int e = max(old, ve);
+                            if (ve < 0) {
+#pragma unroll 1
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint32_t bits = live ? seen(c) : 0u;
+                                    if (bits == 0xFFFFu) e = max(e, static_cast<int>(sm->vgroup[sc][c]));
+                                    if (__any_sync(0xffffffffu, bits != 0u && bits != 0xFFFFu)) {
+#pragma unroll
+                                        for (int i = 0; i < 16; ++i) {
+                                            const int x = (__float_as_uint(sm->vs[sc][16 * c + i]) >> 23) & 255;
+                                            if (((bits >> i) & 1) && x != 255) e = max(e, x);
+                                        }
+                                    }
+                                }
+                            }
+                            if (__any_sync(0xffffffffu, e != old)) {
+                                ok = rescale(pow2i(max(-126, old - e)), 0);
+                                if (!ok) break;
+                            }
+                            const int first = __shfl_sync(0xffffffffu, e, 0);
+                            vcur = __all_sync(0xffffffffu, !live || e == first) ? first : -1;
+                            sm->row_vexp[t][row] = e;
+                            own_ref = ve < 0 || vcur != ve;
                         }
                         if (__any_sync(0xffffffffu, m == kNone)) {
                             // Rows that have seen nothing yet start from their largest score.
@@ -699,43 +743,54 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                             }
                             if (m == kNone) m = fmaxf(m, top * fr);
                         }
-                        // One pass with the maximum as it is.  Where a score exceeds it by more
-                        // than 2^8 (seldom), it moves by a whole number, so that what is done
-                        // already (sums, weights, O) is rescaled exactly.  (A sum of weights up
-                        // to 2^8 has none above it.)
-                        auto weigh = [&](auto cut_tag) {
-                            constexpr bool kCut = decltype(cut_tag)::value;
+                        // One pass with the maximum as it is, where the warp's rows see the whole step and
+                        // have its reference.
+                        float lsum = 0.f;
+                        int c0 = 0;  // chunks of 16 tokens done
+                        if (!cut && !own_ref) {
                             uint32_t s[16];
                             tmem_ld16(s_col, s);
-                            float lsum = 0.f;
-#pragma unroll(kCut ? 1 : 8)
-                            for (int c = 0; c < 8; ++c) {
-                                ulonglong2 k[4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) k[i] = ks2[4 * c + i];
-                                const uint64_t m2 = pack2(-m, -m);
+                            for (int c = 0; c < 8; ++c) {
                                 uint64_t y[8], l2 = 0;
                                 uint32_t p[8];
-                                tmem_wait_ld16(s);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    y[2 * i] = fma2(mul2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k[i].x), fr2, m2);
-                                    y[2 * i + 1] = fma2(mul2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k[i].y), fr2, m2);
+                                bases(s, c, y, [&] {
+                                    if (c < 7) tmem_ld16(s_col + 16 * (c + 1), s);
+                                });
+                                weights(y, c, l2, p, std::false_type());
+                                const float sum = unpack2(l2).x + unpack2(l2).y;
+                                if (__any_sync(0xffffffffu, sum > 256.f)) {  // seldom
+                                    if (c < 7) tmem_wait_ld16(s);
+                                    break;
                                 }
-                                if (c < 7) tmem_ld16(s_col + 16 * (c + 1), s);
-                                const uint32_t bits = kCut ? seen(c) : 0xFFFFu;
-                                if (kCut) {
+                                lsum += sum;
+                                tmem_st8(s_col + 8 * c, p);
+                                c0 = c + 1;
+                            }
+                        }
+                        // The rest, and steps with masks or references of the rows' own.  Where a score
+                        // exceeds the maximum by more than 2^8, it moves by a whole number, so that what
+                        // is done already (sums, weights, O) is rescaled exactly.  (A sum of weights up
+                        // to 2^8 has none above it.)
+                        if (c0 < 8) {
+                            const float g = own_ref ? pow2i(max(-126, (ve < 0 ? 133 : ve) - sm->row_vexp[t][row])) : 1.f;
+#pragma unroll 1
+                            for (int c = c0; c < 8; ++c) {
+                                uint32_t s[16];
+                                tmem_ld16(s_col + 16 * c, s);
+                                uint64_t y[8], l2 = 0;
+                                uint32_t p[8];
+                                bases(s, c, y, [] {});
+                                const uint32_t bits = seen(c);
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        const float2 z = unpack2(y[i]);
-                                        y[i] = pack2((bits >> (2 * i)) & 1 ? z.x : -INFINITY,
-                                                     (bits >> (2 * i)) & 2 ? z.y : -INFINITY);
-                                    }
+                                for (int i = 0; i < 8; ++i) {
+                                    const float2 z = unpack2(y[i]);
+                                    y[i] = pack2((bits >> (2 * i)) & 1 ? z.x : -INFINITY,
+                                                 (bits >> (2 * i)) & 2 ? z.y : -INFINITY);
                                 }
-                                weights(y, c, l2, p);
+                                weights(y, c, l2, p, g);
                                 float sum = unpack2(l2).x + unpack2(l2).y;
                                 if (__any_sync(0xffffffffu, sum > 256.f)) {
-                                    if (c < 7) tmem_wait_ld16(s);  // the next scores: not in flight below
                                     float top = 0.f;
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(unpack2(y[i]).x, unpack2(y[i]).y));
@@ -746,26 +801,23 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) y[i] = add2(y[i], pack2(-up, -up));
                                     ok = rescale(f, 8 * c);
-                                    if (!ok) return;
+                                    if (!ok) break;
                                     l2 = 0;
-                                    weights(y, c, l2, p);
+                                    weights(y, c, l2, p, g);
                                     sum = unpack2(l2).x + unpack2(l2).y;
                                 }
-                                if (kCut) {  // unseen: exactly zero, whatever the value row's scale is
+                                // unseen: exactly zero, whatever the value row's scale is
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        const uint32_t two = (bits >> (2 * i)) & 3u;
-                                        p[i] &= (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
-                                    }
+                                for (int i = 0; i < 8; ++i) {
+                                    const uint32_t two = (bits >> (2 * i)) & 3u;
+                                    p[i] &= (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
                                 }
                                 lsum += sum;
-                                if (kCut) __syncwarp();
+                                __syncwarp();
                                 tmem_st8(s_col + 8 * c, p);
                             }
-                            l += lsum;
-                        };
-                        if (cut) weigh(std::true_type());
-                        else weigh(std::false_type());
+                        }
+                        l += lsum;
                         if (!ok) break;
                         tmem_wait_st();
                     }
@@ -804,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             } else {
                 weight = l == 0.f ? 0.f : 1.f / l;
             }
-            const float vback = pow2i(vcur - 133);
+            const float vback = pow2i((vcur < 0 ? sm->row_vexp[t][row] : vcur) - 133);
             auto output = [&](auto add) {  // the row's normalized output, in chunks of 32 dims
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -1076,12 +1128,21 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         // =============================== scales ===============================
         // Page numbers are read one step before the words' copies are issued, and
         // those (cp.async, each lane its own words) kScaleAhead steps before use.
-        int pj = 0, kv0 = 0, lo = 0, hi = 0, h = 0, id[4], vexp = 7;
-        bool fetched = more, opens = false;  // a step's page numbers are at hand; it opens a segment
+        int pj = 0, kv0 = 0, lo = 0, hi = 0, h = 0, id[4];
+        uint32_t vexp = 7, flags = 0;
+        int all_lo = 0, all_hi = 0;  // positions that all rows of the item see
+        bool fetched = more;  // a step's page numbers are at hand
         uint32_t issued = 0;
         auto fetch_pages = [&]() {
             kv0 = w.lo + (w.u0 + pj) * kStep, lo = w.s.lo, hi = w.hi, h = w.h;
-            opens = pj == 0;
+            flags = 0;
+            if (pj == 0) {
+                flags = kOpens;
+                all_hi = a.causal ? min(hi, w.s.first + w.r0 / a.group + 1) : hi;
+                all_lo = a.window > 0 ? max(lo, w.s.first + (w.r0 + w.R - 1) / a.group + 1 - a.window) : lo;
+            }
+            flags |= static_cast<uint32_t>(min(max(all_lo - kv0, 0), kStep)) << kFrom;
+            flags |= static_cast<uint32_t>(min(max(all_hi - kv0, 0), kStep)) << kTo;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int tile = (kv0 + 32 * i + lane) >> 4;
@@ -1113,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
                                      smem_u32(&sm->word[rs][1][32 * i + lane])), "l"(a.c.vs + rr), "r"(n) : "memory");
                 }
-                if (lane == 0) sm->word_bad[rs] = badbits | (opens ? 1u << 31 : 0u);
+                if (lane == 0) sm->word_info[rs] = badbits | flags;
                 fetched = more;
                 if (fetched) fetch_pages();
             }
@@ -1127,18 +1188,27 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             const int sc = step_no % kScaleStages, rs = step_no % (kScaleAhead + 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(kScaleAhead) : "memory");
             __syncwarp();
-            const uint32_t info = sm->word_bad[rs];
-            uint32_t kw[4], vw[4], ve = 0;
+            const uint32_t info = sm->word_info[rs];
+            const int from = (info >> kFrom) & 255u, to = (info >> kTo) & 255u;
+            uint32_t kw[4], vw[4], e[4], top = 7, common = 7;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kw[i] = sm->word[rs][0][32 * i + lane];
                 vw[i] = sm->word[rs][1][32 * i + lane];
-                const uint32_t e = (vw[i] >> 23) & 255u;
-                ve = max(ve, e == 255u ? 0u : e);
+                e[i] = (vw[i] >> 23) & 255u;
+                if (e[i] == 255u) e[i] = 0;
+                top = max(top, e[i]);
+                if (32 * i + lane >= from && 32 * i + lane < to) common = max(common, e[i]);
             }
-            // of the item's part: the streams start anew with each
-            vexp = max(info >> 31 ? 7 : vexp, static_cast<int>(__reduce_max_sync(0xffffffffu, ve)));
-            const float vmul = pow2i(133 - vexp);
+            vexp = max(info & kOpens ? 7u : vexp, __reduce_max_sync(0xffffffffu, common));
+            const bool own_ref = __reduce_max_sync(0xffffffffu, top) > vexp;
+            const float vmul = own_ref ? 1.f : pow2i(133 - static_cast<int>(vexp));
+            if (own_ref) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) e[i] = max(e[i], __shfl_xor_sync(0xffffffffu, e[i], o));
+            }
             if (!__all_sync(0xffffffffu, bar_wait(smem_u32(&sm->sc_empty[sc]),
                                                    ((step_no / kScaleStages) & 1) ^ 1, abort_flag, a.status)))
                 break;
@@ -1148,9 +1218,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                 const float v = FMT == W4KV_INT4 ? int4_scale(vw[i]) : __uint_as_float(vw[i]);
                 sm->ks[sc][32 * i + lane] = k * a.scale_log2;
                 sm->vs[sc][32 * i + lane] = v * vmul;
+                if ((lane & 15) == 0) sm->vgroup[sc][2 * i + (lane >> 4)] = static_cast<uint8_t>(e[i]);
             }
             if (lane == 0) {
-                sm->vexp[sc] = vexp;
+                sm->vexp[sc] = own_ref ? -1 : static_cast<int>(vexp);
                 sm->bad[sc] = info & 255u;
                 if (info & 255u) atomicOr(a.status, kStatusBounds);
             }
