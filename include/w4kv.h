@@ -21,7 +21,9 @@
  *   W4KV_INT8  s = fl32(amax / 127), q = clamp(rne(fl32(x / s)), -127, 127);
  *              the row stands for q * s.
  *   W4KV_E4M3  s = fl32(amax / 448), q = the nearest E4M3 value (ties to even,
- *              saturating) of fl32(x / s); the row stands for q * s.
+ *              saturating) of fl32(x / s); the row stands for q * s.  (The NaN
+ *              codes 0x7F and 0xFF, which w4kv_append does not write, stand for
+ *              NaN in their element.)
  *   W4KV_INT4  lo = min(0, min x), hi = max(0, max x); s = fl32(fl32(hi - lo) / 15)
  *              with its bit pattern rounded to a multiple of 16 (ties up);
  *              z = rne(fl32(-lo / s)), u = clamp(rne(fl32(fl32(x / s) + z)), 0, 15).

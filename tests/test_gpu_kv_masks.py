@@ -173,3 +173,55 @@ def test_value_sizes_per_row(w4, fmt, n, H, window, copies):
         O, lse = w4.w4kv_attention(Q.cuda().repeat(copies, 1, 1), p.device(w4), *shared(p, n, copies),
                                    max_rows=n, window=window, return_lse=True)
         close_copies(O, lse, row_tolerance(p, Q, [n], D ** -0.5, True, window), copies)
+
+
+@pytest.mark.parametrize("D", (64, 128))
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("n,H", [(1, 2), (1, 16)] + SHAPES)
+def test_nan_codes(w4, n, H, dtype, D):
+    """E4M3's NaN codes: in a value they make that element of the rows that see
+    it NaN, in a key all of those rows, and nothing else changes."""
+    L = 400
+    p = R.Plain([L], R.E4M3, 2, D, 16, 1)
+    Q = rows((n, H, D), dtype, 2).cuda()
+    batch = p.batch([n])
+    for at, window in UNSEEN + [(L - n // 2 - 1, 0), (3, 0), (L - 1, 1), (L - n, 5)]:
+        want = w4.w4kv_attention(Q, p.device(w4), *batch, window=window)
+        sees = token_rows(L, n, at, window).cuda()
+        pg, off = (int(x) for x in p.at(0, at))
+        for dim, code in ((0, 0x7F), (D - 1, 0xFF), (D // 2 + 5, 0x7F)):
+            bad = p.device(w4)
+            bad.v_codes[pg, 0, off, dim] = code
+            got = w4.w4kv_attention(Q, bad, *batch, window=window)
+            assert torch.equal(got[~sees], want[~sees]), (at, window, dim)
+            assert torch.isnan(got[sees, :H // 2, dim]).all(), (at, window, dim)
+            got[sees, :H // 2, dim] = want[sees, :H // 2, dim]
+            assert torch.equal(got, want), (at, window, dim)
+        bad = p.device(w4)
+        bad.k_codes[pg, 0, off, 7] = 0x7F
+        got = w4.w4kv_attention(Q, bad, *batch, window=window)
+        assert torch.isnan(got[sees, :H // 2]).all()
+        got[sees, :H // 2] = want[sees, :H // 2]
+        assert torch.equal(got, want), (at, window)
+
+
+def test_nan_codes_in_long_and_cut_items(w4):
+    """NaN codes in many places of a long sequence whose items several blocks share."""
+    L, D, n, H = 3000, 128, 300, 2
+    p = R.Plain([L] * 12, R.E4M3, 1, D, 16, 1)
+    Q = rows((12 * n, H, D), torch.bfloat16, 2).cuda()
+    batch = p.batch([n] * 12)
+    r = np.random.default_rng(1)
+    for window in (0, 200, 1000):
+        want = w4.w4kv_attention(Q, p.device(w4), *batch, max_rows=n, window=window)
+        bad = p.device(w4)
+        nan = torch.zeros((12 * n, D), dtype=torch.bool)
+        for at in list(r.integers(2600, L, 40)) + list(r.integers(1500, 2600, 10)):
+            b, dim = int(r.integers(12)), int(r.integers(D))
+            pg, off = (int(x) for x in p.at(b, int(at)))
+            bad.v_codes[pg, 0, off, dim] = 0xFF
+            nan[b * n:(b + 1) * n, dim] |= token_rows(L, n, int(at), window)
+        got = w4.w4kv_attention(Q, bad, *batch, max_rows=n, window=window)
+        nan = nan[:, None].expand(12 * n, H, D).cuda()
+        assert torch.equal(torch.isnan(got), nan)
+        assert torch.equal(got[~nan], want[~nan])

@@ -106,6 +106,25 @@ __device__ __forceinline__ float pow2i(int e) {  // 2^e, -126 <= e <= 127
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// The NaN codes (0x7F, 0xFF) of four E4M3 codes: bit 7 of their bytes.
+__device__ __forceinline__ uint32_t e4m3_nans(uint32_t w) {
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// Zeros in place of the NaN codes of `bytes` bytes (a lane's words from `at` on, 128 apart);
+// *found = 1 if there was one.  A call, so that it costs the loop that seldom needs it little.
+inline __device__ __noinline__ void zero_nans(uint32_t *at, int bytes, int *found) {
+#pragma unroll 1
+    for (int i = 0; i < bytes / 4; i += 32) {
+        const uint32_t n = e4m3_nans(at[i]);
+        if (n) {
+            at[i] &= ~((n >> 7) * 255u);
+            *found = 1;
+        }
+    }
+    __syncwarp();
+}
+
 // a / b, by 32 bits where they do.
 __device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);

@@ -64,7 +64,7 @@ struct Shape {
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kJoin = kWarps * kTileRows * kPad * 4;
     static constexpr int kStats = kWarps * kTileRows * 2 * 4;
-    static constexpr int kSmem = kRing + kJoin + kStats + static_cast<int>(sizeof(RangeSmem)) + 16;
+    static constexpr int kSmem = kRing + kJoin + kStats + static_cast<int>(sizeof(RangeSmem)) + 32;
     // the grid is one wave: kBlocks of them (and 1 KB each) fit an SM's 228 KB
     static_assert(kBlocks * (kSmem + 1024) <= 228 * 1024, "shared memory");
 };
@@ -185,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
     float *stat_l = stat_m + kWarps * S::kTileRows;
     RangeSmem *rsm = reinterpret_cast<RangeSmem *>(
         smem + ((S::kRing + S::kJoin + S::kStats + 15) & ~15));
+    int *nans = reinterpret_cast<int *>(rsm + 1);  // a value's NaN code has been taken out: see zero_nans
+    if (FMT == W4KV_E4M3 && threadIdx.x == 0) *nans = 0;  // (barriers follow)
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     auto tiles_of = [&](const Seq &s) { return (s.n * a.group - 1) / S::kTileRows + 1; };
@@ -542,6 +544,11 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 }
             }
             // ---- O^T += V^T P^T ----
+            // A weight of zero times a NaN is a NaN: in cut tiles, whose tokens not all rows see, NaN
+            // codes count as zeros, and at the item's end each row looks for those it sees.
+            if (FMT == W4KV_E4M3 && cut)
+                zero_nans(reinterpret_cast<uint32_t *>(ring + get * S::kStage + kTile * S::kRow) + lane,
+                          kTile * S::kRow, nans);
             uint32_t vw[4][S::kVB / 4];
             uint32_t vz[2];  // zero points of the value rows 2c, 2c + 1 and 2c + 8, 2c + 9
 #pragma unroll
@@ -712,6 +719,20 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                     y += v.y;
                 }
                 const int d = (D / 8) * (j & 7) + 2 * (ph * kT + (j >> 3));
+                if (FMT == W4KV_E4M3 && *nans) {  // the row's NaN codes in cut tiles
+                    const int pos = w.s.first + (r0 + r) / a.group;
+                    const int from = max(a.window > 0 ? pos + 1 - a.window : 0, (w.lo / 16 + w.u0 * (kUnit / 16)) * 16);
+                    const int to = min(min(w.hi, a.causal ? pos + 1 : w.hi), (w.lo / 16 + w.u1 * (kUnit / 16)) * 16);
+                    for (int at = max(from, w.lo); at < to; ++at) {
+                        if (at >= ((all_lo + 15) & ~15) && at < (all_hi & ~15)) at = all_hi & ~15;
+                        const int64_t row = at < to ? row_of(a.c, a.b, w.b, at) : -1;
+                        if (row < 0) continue;
+                        const uint32_t code = __ldg(reinterpret_cast<const uint16_t *>(
+                            a.c.v + (row + int64_t(w.h) * a.c.page) * D + d));
+                        if (e4m3_nans(code) & 0x80u) x = __uint_as_float(0x7FC00000u);
+                        if (e4m3_nans(code) & 0x8000u) y = __uint_as_float(0x7FC00000u);
+                    }
+                }
                 if (whole) {
                     const int t = (r0 + r) / a.group;
                     *reinterpret_cast<uint32_t *>(a.o + int64_t(w.s.row0 + t) * a.o_row +

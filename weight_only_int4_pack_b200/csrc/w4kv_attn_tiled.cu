@@ -167,6 +167,13 @@ __device__ __forceinline__ int own_steps(const Attn &a, const Walk &w, int t) {
     return w.R <= kM ? (w.u1 - w.u0 + 1 - t) >> 1 : stream_steps(a, w, t);
 }
 
+// Positions of the item that all its rows see.
+__device__ __forceinline__ void common_bounds(const Attn &a, const Walk &w, int *lo, int *hi) {
+    *hi = a.causal ? min(w.hi, w.s.first + w.r0 / a.group + 1) : w.hi;
+    *lo = w.s.lo;
+    if (a.window > 0) *lo = max(*lo, w.s.first + (w.r0 + w.R - 1) / a.group + 1 - a.window);
+}
+
 // The warp's walk in shared memory, moved by lane 0.
 __device__ __forceinline__ bool warp_next(const Attn &a, Walk *w) {
     __syncwarp();
@@ -201,6 +208,7 @@ struct alignas(16) Control {
     RangeSmem range;
     uint32_t tmem;
     int abort_flag, mma_lock;
+    int nans;  // a value's NaN code has been taken out: see zero_nans
 };
 
 template <int FMT, int D>
@@ -436,6 +444,25 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
     return r;
 }
 
+// Dims in which a token of [lo, hi) has an E4M3 NaN code in its value: bit i of nan[c] for dim 32 c + i.
+template <int D>
+__device__ __forceinline__ void find_nans(const Attn &a, int b, int h, int lo, int hi, uint32_t (&nan)[D / 32]) {
+#pragma unroll 1
+    for (int at = lo; at < hi; ++at) {
+        const int64_t r = row_of(a.c, a.b, b, at);
+        if (r < 0) continue;
+        const uint4 *code = reinterpret_cast<const uint4 *>(a.c.v + (r + int64_t(h) * a.c.page) * D);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const uint4 v = __ldg(code + i);
+            const uint32_t x[4] = {e4m3_nans(v.x) >> 7, e4m3_nans(v.y) >> 7, e4m3_nans(v.z) >> 7, e4m3_nans(v.w) >> 7};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                nan[i / 2] |= ((x[q] | x[q] >> 7 | x[q] >> 14 | x[q] >> 21) & 15u) << (16 * (i & 1) + 4 * q);
+        }
+    }
+}
+
 // Eight INT4 codes -> u - z in dim order; zb = 1024 + z in both halves.
 __device__ __forceinline__ uint4 widen8_int4(uint32_t w, uint32_t zb) {
     uint4 r;
@@ -476,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         mbar_init(smem_u32(&sm->joined), 2 * kM);
         sm->abort_flag = 0;
         sm->mma_lock = 0;
+        sm->nans = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const Range range = block_range<kThreads>(a.b.n, &sm->range, [&](int b) -> int64_t {
@@ -856,7 +884,24 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             } else {
                 weight = l == 0.f ? 0.f : 1.f / l;
             }
+            uint32_t nan[D / 32] = {};
+            if (FMT == W4KV_E4M3 && __any_sync(0xffffffffu, own > 0 && *static_cast<volatile int *>(&sm->nans))) {
+                int all_lo, all_hi;  // outside them, to multiples of 16, NaN codes count as zeros in the MMAs
+                common_bounds(a, w, &all_lo, &all_hi);
+                const int from = max(clo, kv_base), to = min(chi, kv_base + ns * kStep);
+                all_lo = (all_lo + 15) & ~15;
+                all_hi = max(all_lo, all_hi & ~15);
+                if (live) {
+                    find_nans<D>(a, w.b, w.h, from, min(to, all_lo), nan);
+                    find_nans<D>(a, w.b, w.h, max(from, all_hi), to, nan);
+                }
+                __syncwarp();
+            }
             const float vback = pow2i((vcur < 0 ? sm->row_vexp[t][row] : vcur) - 133);
+            auto value = [&](int d, uint32_t o) {
+                if (FMT == W4KV_E4M3 && ((nan[d / 32] >> (d % 32)) & 1)) return __uint_as_float(0x7FC00000u);
+                return __uint_as_float(o) * weight * vback;
+            };
             auto output = [&](auto add) {  // the row's normalized output, in chunks of 32 dims
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -868,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                     float x[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        x[i] = add(32 * c + i, own > 0 ? __uint_as_float(o[i]) * weight * vback : 0.f);
+                        x[i] = add(32 * c + i, own > 0 ? value(32 * c + i, o[i]) : 0.f);
                     if (live && whole) {
                         uint16_t *op = a.o + int64_t(w.s.row0 + token) * a.o_row + head * a.o_head + 32 * c;
 #pragma unroll
@@ -912,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            joined[(32 * c + i) * kM + row] = own > 0 ? __uint_as_float(o[i]) * weight * vback : 0.f;
+                            joined[(32 * c + i) * kM + row] = own > 0 ? value(32 * c + i, o[i]) : 0.f;
                     }
                 }
                 join();
@@ -931,10 +976,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
         const int wr = (warp - 8) * 16;  // its first row
         uint8_t *ring = base + L::kRaw + (warp - 8) * L::kRawWarp;
         int pj = 0, id = -1, kv0 = 0, hi = 0, lo = 0, h = 0;
+        int all_lo = 0, all_hi = 0;  // positions that all rows of the item see
+        uint32_t part_mask = 0;      // per tile on its way: values that not all rows see
         bool fetched = more;  // a step's page number is at hand
         auto fetch_page = [&]() {
             kv0 = w.lo + (w.u0 + pj) * kStep + wr;
             lo = w.s.lo, hi = w.hi, h = w.h;
+            if (FMT == W4KV_E4M3 && pj == 0) common_bounds(a, w, &all_lo, &all_hi);
             int rest;
             const int pg = page_of_tile(a, kv0 >> 4, &rest);
             id = pg < a.b.width && kv0 < hi ? __ldg(a.b.table + w.b * a.b.stride + pg) : -1;
@@ -965,6 +1013,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 16 * kRow + lane * 4),
                                  "l"((is_v ? a.c.vs : a.c.ks) + rr + lane), "r"(lane >= v0 && lane < v1 ? 4 : 0) : "memory");
                 ++issued;
+                if (FMT == W4KV_E4M3) {
+                    const bool part = is_v && (kv0 < all_lo || kv0 + 16 > all_hi);
+                    part_mask = (part_mask & ~(1u << put)) | static_cast<uint32_t>(part) << put;
+                }
                 if (is_v) {
                     fetched = more;
                     if (fetched) fetch_page();
@@ -986,6 +1038,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             asm volatile("cp.async.wait_group %0;" ::"n"(L::kRawTiles - 1) : "memory");
             __syncwarp();
             const uint8_t *src = ring + get * L::kRawTile;
+            // A weight of zero times a NaN is a NaN: among values that not all rows see, NaN codes
+            // count as zeros, and the softmax warps look which rows see them at the item's end.
+            if (FMT == W4KV_E4M3 && ((part_mask >> get) & 1))
+                zero_nans(reinterpret_cast<uint32_t *>(ring + get * L::kRawTile) + lane, 16 * kRow, &sm->nans);
             uint2 raw[kN];
             uint32_t z[kN];
 #pragma unroll
@@ -1138,8 +1194,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             flags = 0;
             if (pj == 0) {
                 flags = kOpens;
-                all_hi = a.causal ? min(hi, w.s.first + w.r0 / a.group + 1) : hi;
-                all_lo = a.window > 0 ? max(lo, w.s.first + (w.r0 + w.R - 1) / a.group + 1 - a.window) : lo;
+                common_bounds(a, w, &all_lo, &all_hi);
             }
             flags |= static_cast<uint32_t>(min(max(all_lo - kv0, 0), kStep)) << kFrom;
             flags |= static_cast<uint32_t>(min(max(all_hi - kv0, 0), kStep)) << kTo;
