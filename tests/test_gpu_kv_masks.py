@@ -225,3 +225,27 @@ def test_nan_codes_in_long_and_cut_items(w4):
         nan = nan[:, None].expand(12 * n, H, D).cuda()
         assert torch.equal(torch.isnan(got), nan)
         assert torch.equal(got[~nan], want[~nan])
+
+
+# ---- scores far below zero --------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", (64, 128))
+@pytest.mark.parametrize("n,H,L", [(1, 2, 1), (1, 2, 300), (5, 8, 40), (90, 2, 200), (150, 4, 300)])
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_scores_below_any_reference(w4, fmt, n, H, L, D):
+    """Keys of 1e33, all alike and against the queries: the rows see their
+    tokens, and weigh them alike."""
+    p = R.Plain([L], fmt, 1, D, 16, 1, dtype=torch.bfloat16)
+    key = np.full((L, 1, D), -1e33, np.float32)
+    p.store(0, 0, 0, *R.quantize(key, fmt))
+    Q = torch.ones((n, H, D), dtype=torch.bfloat16)
+    O, lse = w4.w4kv_attention(Q.cuda(), p.device(w4), *p.batch([n]), return_lse=True)
+    k = R.values(*p.rows(0, 0, 0, 1), fmt)[0, 0]
+    v = torch.from_numpy(R.values(*p.rows(1, 0), fmt))[:, 0]
+    u = 2.0 ** -8
+    for i in range(n):
+        seen = v[:L - n + i + 1]
+        mean, size = seen.mean(0), seen.abs().mean(0)
+        tol = u * mean.abs() + (1 + u) * size * (2.0 ** -11 + (L + 8) * 2.0 ** -23 + 2.0 ** -20)
+        assert ((O[i].cpu().double() - mean).abs() <= tol + L * 2.0 ** -30 * seen.abs().max()).all()
+    assert ((lse.cpu().double() / (k.sum() * D ** -0.5) - 1).abs() <= (D + 16) * 2.0 ** -23).all()

@@ -13,6 +13,8 @@
 // over the sequences, then a scan of the 256 that hold its first unit.
 #pragma once
 
+#include <float.h>
+
 #include <atomic>
 
 #include "w4kv.cuh"
@@ -219,9 +221,9 @@ __device__ __forceinline__ int block_of_unit(int64_t u, const Range &r) {
     return static_cast<int>(div_small((u + 1) * r.blocks - 1, r.total));
 }
 
-// Reference maximum of a row that has seen nothing: below every score, and
-// finite, so that differences of maxima are numbers.
-constexpr float kNone = -1e30f;
+// Reference maximum of a row that has seen nothing: the least finite number, so
+// that no score is below it and differences of equal maxima are numbers.
+constexpr float kNone = -FLT_MAX;
 
 // A partial result: maxima and sums (base 2) and the normalized output of
 // `rows` rows: [rows] + [rows] + [rows][dim] floats (the tiled kernel's output:
