@@ -249,3 +249,22 @@ def test_scores_below_any_reference(w4, fmt, n, H, L, D):
         tol = u * mean.abs() + (1 + u) * size * (2.0 ** -11 + (L + 8) * 2.0 ** -23 + 2.0 ** -20)
         assert ((O[i].cpu().double() - mean).abs() <= tol + L * 2.0 ** -30 * seen.abs().max()).all()
     assert ((lse.cpu().double() / (k.sum() * D ** -0.5) - 1).abs() <= (D + 16) * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("size", [3e3, 1e5, 1e8, 1e20, 1e33])
+@pytest.mark.parametrize("n,H", [(3, 2), (20, 4), (40, 4), (300, 4)])
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_first_tokens_of_no_weight(w4, fmt, n, H, size):
+    """Many first tokens with scores far below the others: they weigh nothing,
+    and the others as if they were alone."""
+    L, D, far = 900, 64, 500
+    p = R.Plain([L], fmt, 2, D, 16, 1, dtype=torch.bfloat16)
+    Q = rows((n, H, D), torch.bfloat16, 2)
+    Q[..., :8] = Q[..., :8].abs() + 0.5
+    key = np.zeros((far, 2, D), np.float32)
+    key[..., :8] = -size
+    p.store(0, 0, 0, *R.quantize(key, fmt))
+    for copies in COPIES:
+        O, lse = w4.w4kv_attention(Q.cuda().repeat(copies, 1, 1), p.device(w4), *shared(p, n, copies),
+                                   max_rows=n, return_lse=True)
+        close_copies(O, lse, R.attention(p, Q, [n], D ** -0.5, unseen=[(0, j) for j in range(far)]), copies)

@@ -798,10 +798,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                         }
                         // The rest, and steps with masks or references of the rows' own.  Where a score
                         // exceeds the maximum by more than 2^8, it moves by a whole number, so that what
-                        // is done already (sums, weights, O) is rescaled exactly.  (A sum of weights up
-                        // to 2^8 has none above it.)
+                        // is done already (sums, weights, O) is rescaled exactly; from far below (where
+                        // that leaves nothing of it) to the largest score itself, whose distance has few
+                        // bits for the fraction.  (A sum of weights up to 2^8 has none above it.)
                         if (c0 < 8) {
                             const float g = own_ref ? pow2i(max(-126, (ve < 0 ? 133 : ve) - sm->row_vexp[t][row])) : 1.f;
+                            int tries = 0;
+                            bool far = false;
 #pragma unroll 1
                             for (int c = c0; c < 8; ++c) {
                                 uint32_t s[16];
@@ -817,23 +820,29 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                                  (bits >> (2 * i)) & 2 ? z.y : -INFINITY);
                                 }
                                 weights(y, c, l2, p, g);
-                                float sum = unpack2(l2).x + unpack2(l2).y;
-                                if (__any_sync(0xffffffffu, sum > 256.f)) {
-                                    float top = 0.f;
+                                const float sum = unpack2(l2).x + unpack2(l2).y;
+                                if (__any_sync(0xffffffffu, far || sum > 256.f) && tries < 4) {
+                                    float top = kNone;
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(unpack2(y[i]).x, unpack2(y[i]).y));
-                                    const float up = sum > 256.f ? ceilf(top) : 0.f, f = ex2(-up);
-                                    m += up;
+                                    float f = 1.f;
+                                    if (far) {
+                                        m = top;
+                                    } else if (sum > 256.f) {
+                                        const float up = ceilf(top);
+                                        f = ex2(-up);
+                                        m = up < 1024.f ? m + up : 0.f;
+                                    }
+                                    far = !far && f < 0x1p-126f;
                                     l *= f;
                                     lsum *= f;
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) y[i] = add2(y[i], pack2(-up, -up));
                                     ok = rescale(f, 8 * c);
                                     if (!ok) break;
-                                    l2 = 0;
-                                    weights(y, c, l2, p, g);
-                                    sum = unpack2(l2).x + unpack2(l2).y;
+                                    ++tries;
+                                    --c;  // the chunk again
+                                    continue;
                                 }
+                                tries = 0;
                                 // unseen: exactly zero, whatever the value row's scale is
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
