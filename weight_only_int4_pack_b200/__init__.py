@@ -557,6 +557,7 @@ class W4KVCache:
         self._c = ctypes.pointer(_CCache(k_codes.data_ptr(), k_scales.data_ptr(),
                                          v_codes.data_ptr(), v_scales.data_ptr(), self.num_pages,
                                          self.page_size, self.kv_heads, self.head_dim, fmt))
+        self._need = {}  # workspace bytes of w4kv_attention by the sizes of a call
 
 
 def w4kv_cache_empty(num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int,
@@ -668,9 +669,6 @@ def w4kv_attention_workspace_bytes(cache: W4KVCache, batch: int, rows: int, max_
                                                      int(max_rows), int(heads)))
 
 
-_kv_need = {}
-
-
 def w4kv_attention(Q, cache: W4KVCache, page_table, kv_lens, cu_rows, max_rows=None, scale=None,
                    causal: bool = True, window: int = 0, out=None, return_lse: bool = False,
                    workspace=None, stream=None):
@@ -701,14 +699,17 @@ def w4kv_attention(Q, cache: W4KVCache, page_table, kv_lens, cu_rows, max_rows=N
     lib = load()
     ws = workspace
     if ws is None:
-        # the size depends on the shapes and the device alone
-        key = (dev.index, cache.kv_heads, cache.head_dim, page_table.shape[0] > 1, rows, max_rows, heads)
-        need = _kv_need.get(key)
+        # the size depends on the cache, its device and these alone
+        key = (min(page_table.shape[0], 2), min(rows, max_rows), heads)
+        need = cache._need.get(key)
         if need is None:
             with torch.cuda.device(dev.index):
                 need = int(lib.w4kv_attention_workspace_bytes(cache._c, page_table.shape[0], rows,
                                                               max_rows, heads))
-            _kv_need[key] = need
+            if need:  # 0: nothing to do, or sizes that the call refuses
+                if len(cache._need) >= 256:
+                    cache._need.clear()
+                cache._need[key] = need
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         size = need
     else:
