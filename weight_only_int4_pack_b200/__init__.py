@@ -620,12 +620,19 @@ def _kv_call(name, cache, stream, fn, *args):
         raise W4Error(name, st)
 
 
-def _kv_made(stream, *tensors):
-    """Tells the allocator that an explicit stream uses tensors made for a call."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _kv_empty(shape, dtype, device, stream, scratch=False):
+    """torch.empty for a call on `stream`: of that stream's memory (what the
+    current stream has let go it may still be reading), kept from reuse, unless
+    it is scratch, until the current stream has passed the tensor's end."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if stream.device != device:
+        raise ValueError("stream must belong to the cache's device")
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def w4kv_append(K, V, cache: W4KVCache, page_table, kv_lens, cu_rows, stream=None) -> None:
@@ -648,9 +655,8 @@ def w4kv_read(cache: W4KVCache, page_table, kv_lens, cu_rows, rows: int, dtype=t
     beyond it are left as they are).  `out` is an optional pair of tensors."""
     if out is None:
         shape = (rows, cache.kv_heads, cache.head_dim)
-        K = torch.empty(shape, dtype=dtype, device=cache.device)
-        V = torch.empty(shape, dtype=dtype, device=cache.device)
-        _kv_made(stream, K, V)
+        K = _kv_empty(shape, dtype, cache.device, stream)
+        V = _kv_empty(shape, dtype, cache.device, stream)
     else:
         K, V = out
         if K.dtype != V.dtype or K.shape[0] != rows or V.shape[0] != rows:
@@ -687,11 +693,11 @@ def w4kv_attention(Q, cache: W4KVCache, page_table, kv_lens, cu_rows, max_rows=N
     qrs, qhs = _kv_rows(Q, cache, heads, "Q")
     O = out
     if O is None:
-        O = torch.empty((rows, heads, cache.head_dim), dtype=Q.dtype, device=dev)
+        O = _kv_empty((rows, heads, cache.head_dim), Q.dtype, dev, stream)
     elif O.dtype != Q.dtype or O.shape[0] != rows:
         raise ValueError("out must have Q's dtype and rows")
     ors, ohs = _kv_rows(O, cache, heads, "out")
-    lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
+    lse = _kv_empty((rows, heads), torch.float32, dev, stream) if return_lse else None
     b = _kv_batch(cache, page_table, kv_lens, cu_rows)
     max_rows = max(rows, 1) if max_rows is None else int(max_rows)
     if scale is None:
@@ -710,14 +716,12 @@ def w4kv_attention(Q, cache: W4KVCache, page_table, kv_lens, cu_rows, max_rows=N
                 if len(cache._need) >= 256:
                     cache._need.clear()
                 cache._need[key] = need
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        ws = _kv_empty(need, torch.uint8, dev, stream, scratch=True) if need else None
         size = need
     else:
         if ws.device != dev or not ws.is_contiguous():
             raise ValueError("workspace must be contiguous on the cache's device")
         size = ws.numel() * ws.element_size()
-    if stream is not None:
-        _kv_made(stream, O if out is None else None, lse, ws if workspace is None else None)
     _kv_call("w4kv_attention", cache, stream, lib.w4kv_attention, cache._c, b, Q.data_ptr(), _dt(Q),
              rows, heads, qrs, qhs, O.data_ptr(), ors, ohs, None if lse is None else lse.data_ptr(),
              max_rows, float(scale), int(bool(causal)), int(window),
