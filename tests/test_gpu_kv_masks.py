@@ -268,3 +268,16 @@ def test_first_tokens_of_no_weight(w4, fmt, n, H, size):
         O, lse = w4.w4kv_attention(Q.cuda().repeat(copies, 1, 1), p.device(w4), *shared(p, n, copies),
                                    max_rows=n, return_lse=True)
         close_copies(O, lse, R.attention(p, Q, [n], D ** -0.5, unseen=[(0, j) for j in range(far)]), copies)
+
+
+# ---- windows that reach beyond every position ---------------------------------------------------
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 20, 2 ** 31, 2 ** 40])
+@pytest.mark.parametrize("n", [3, 40, 150])
+def test_windows_of_31_bits(w4, n, window):
+    """The longest windows are none, for rows before the first position too."""
+    p = R.Plain([2, n - 1, 200], R.INT8, 1, 64, 16, 1)
+    Q = rows((3 * n, 2, 64), torch.float16, 3).cuda()
+    batch = p.batch([n, n, n])
+    want = w4.w4kv_attention(Q, p.device(w4), *batch)
+    assert torch.equal(w4.w4kv_attention(Q, p.device(w4), *batch, window=window), want)

@@ -47,6 +47,11 @@ struct Attn {
     unsigned *status;
 };
 
+// The first position that a row at `pos` sees through a window: pos + 1 - window, at least 0.
+__device__ __forceinline__ int window_from(int pos, int window) {
+    return pos >= window ? pos + 1 - window : 0;
+}
+
 // The rows that a launch serves of a sequence, and the cached positions they see.
 struct Seq {
     int row0, n;  // first row of the call, rows served (0: not served by this launch)
@@ -82,7 +87,7 @@ __device__ __forceinline__ Seq load_seq(const Attn &a, int b) {
         atomicOr(a.status, kStatusBounds);
         s.hi = room;
     }
-    if (a.window > 0) s.lo = min(s.hi, max(0, s.first + 1 - a.window));
+    if (a.window > 0) s.lo = min(s.hi, window_from(s.first, a.window));
     return s;
 }
 

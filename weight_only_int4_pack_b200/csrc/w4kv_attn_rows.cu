@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
     auto tile_range = [&](const Seq &s, int tile, int *lo, int *hi) {
         const int r0 = tile * S::kTileRows, r1 = min(s.n * a.group, r0 + S::kTileRows) - 1;
         *hi = a.causal ? min(s.hi, max(0, s.first + r1 / a.group + 1)) : s.hi;
-        *lo = a.window > 0 ? min(*hi, max(0, s.first + r0 / a.group + 1 - a.window)) : 0;
+        *lo = a.window > 0 ? min(*hi, window_from(s.first + r0 / a.group, a.window)) : 0;
         return max(1, ((*hi + 15) / 16 - *lo / 16 + kUnit / 16 - 1) / (kUnit / 16));  // units
     };
     const Range range = block_range<kThreads>(a.b.n, rsm, [&](int b) -> int64_t {
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
         }
         // tiles inside [all_lo, all_hi) are seen whole by every row
         const int all_hi = a.causal ? min(w.hi, w.s.first + r0 / a.group + 1) : w.hi;
-        const int all_lo = a.window > 0 ? max(w.lo, w.s.first + (r0 + R - 1) / a.group + 1 - a.window) : w.lo;
+        const int all_lo = a.window > 0 ? max(w.lo, window_from(w.s.first + (r0 + R - 1) / a.group, a.window)) : w.lo;
 
         float m[NT][2], l[NT][2], o[NT][S::kSteps][4];
 #pragma unroll
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                     for (int i = 0; i < 4; ++i) {
                         const int j = kv0 + g + 8 * (i >> 1), pos = qpos[nt][i & 1];
                         if (bad || j < w.lo || j >= w.hi || (a.causal && j > pos) ||
-                            (a.window > 0 && j <= pos - a.window))
+                            (a.window > 0 && j < window_from(pos, a.window)))
                             sc[nt][i] = -INFINITY;
                     }
             }
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FMT, D, NT>::kBlocks) rows_ker
                 const int d = (D / 8) * (j & 7) + 2 * (ph * kT + (j >> 3));
                 if (FMT == W4KV_E4M3 && *nans) {  // the row's NaN codes in cut tiles
                     const int pos = w.s.first + (r0 + r) / a.group;
-                    const int from = max(a.window > 0 ? pos + 1 - a.window : 0, (w.lo / 16 + w.u0 * (kUnit / 16)) * 16);
+                    const int from = max(a.window > 0 ? window_from(pos, a.window) : 0, (w.lo / 16 + w.u0 * (kUnit / 16)) * 16);
                     const int to = min(min(w.hi, a.causal ? pos + 1 : w.hi), (w.lo / 16 + w.u1 * (kUnit / 16)) * 16);
                     for (int at = max(from, w.lo); at < to; ++at) {
                         if (at >= ((all_lo + 15) & ~15) && at < (all_hi & ~15)) at = all_hi & ~15;

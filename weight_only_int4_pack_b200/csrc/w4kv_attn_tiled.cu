@@ -78,7 +78,7 @@ __device__ __forceinline__ void tile_bounds(const Attn &a, const Seq &s, int til
     const int r0 = tile * kTileRows;  // rows * group of a call is below 2^31
     const int r1 = min(s.n * a.group, r0 + kTileRows) - 1;
     *hi = a.causal ? min(s.hi, max(0, s.first + r1 / a.group + 1)) : s.hi;
-    *lo = a.window > 0 ? max(0, s.first + r0 / a.group + 1 - a.window) : 0;
+    *lo = a.window > 0 ? window_from(s.first + r0 / a.group, a.window) : 0;
     *lo = min(*lo, *hi) & ~15;
 }
 
@@ -171,7 +171,7 @@ __device__ __forceinline__ int own_steps(const Attn &a, const Walk &w, int t) {
 __device__ __forceinline__ void common_bounds(const Attn &a, const Walk &w, int *lo, int *hi) {
     *hi = a.causal ? min(w.hi, w.s.first + w.r0 / a.group + 1) : w.hi;
     *lo = w.s.lo;
-    if (a.window > 0) *lo = max(*lo, w.s.first + (w.r0 + w.R - 1) / a.group + 1 - a.window);
+    if (a.window > 0) *lo = max(*lo, window_from(w.s.first + (w.r0 + w.R - 1) / a.group, a.window));
 }
 
 // The warp's walk in shared memory, moved by lane 0.
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
             // ---- what the row sees: [clo, chi); what all rows of the warp see: [all_lo, all_hi) ----
             const int pos = w.s.first + token;
             int clo = w.lo, chi = w.hi;
-            if (a.window > 0) clo = max(clo, pos + 1 - a.window);
+            if (a.window > 0) clo = max(clo, window_from(pos, a.window));
             if (a.causal) chi = min(chi, pos + 1);
             if (!live) clo = w.lo, chi = w.hi;
             clo = max(clo, w.s.lo);
