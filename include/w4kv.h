@@ -48,6 +48,7 @@
  * sequence: nothing of them is read or written.  These arrays live on the
  * device and are read by the kernels, so that one captured graph serves
  * changing lengths.
+ *   table_width * page_size is at most 2^31 - 256.
  *   A position below 0 or beyond table_width pages and a page number outside
  *   [0, num_pages) are never dereferenced: the row is not stored (append),
  *   reads as zeros (read) or counts as unseen (attention), and the device status word

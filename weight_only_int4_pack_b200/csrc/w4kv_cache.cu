@@ -335,8 +335,9 @@ int check_batch(const char *fn, const w4kv_batch *b, const w4kv_cache *c, Batch 
     if (!b) return set_error(W4_ERR_INVALID_ARG, fn, "null batch");
     if (b->batch < 0 || b->batch > (1 << 20))
         return set_error(W4_ERR_INVALID_ARG, fn, "batch must be 0 .. 2^20");
-    if (b->table_width < 1 || b->table_width > 0x7FFFFFFF / c->page_size)
-        return set_error(W4_ERR_INVALID_ARG, fn, "table_width * page_size must be 1 .. 2^31 - 1");
+    // positions are rounded up to units of up to 256 in 31 bits
+    if (b->table_width < 1 || b->table_width > (0x7FFFFFFF - 255) / c->page_size)
+        return set_error(W4_ERR_INVALID_ARG, fn, "table_width * page_size must be 1 .. 2^31 - 256");
     if (b->batch > 1 && b->table_stride < 0)
         return set_error(W4_ERR_INVALID_ARG, fn, "table_stride must not be negative");
     if (b->batch > 0 && (!b->page_table || !b->kv_lens || !b->cu_rows))
