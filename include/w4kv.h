@@ -94,7 +94,8 @@ typedef struct {
  * w4kv_append -- quantizes the keys and values of new tokens into the cache.
  *   K, V  [rows][kv_heads][head_dim] fp16 or bf16 (xt); the strides count
  *         elements, are multiples of 8 and need not be those of a dense array
- *         (slices of a fused projection's output work as they are).
+ *         (slices of a fused projection's output work as they are).  The
+ *         stride of a single row or head is not looked at.
  *   Positions that two rows of one call name (pages shared between sequences)
  *   hold one or the other row, or a mixture: pages that are written belong to
  *   one sequence.

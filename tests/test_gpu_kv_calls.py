@@ -155,3 +155,21 @@ def test_stream_of_no_device_of_the_cache(w4):
     Q = rows((1, 1, 64), torch.float16, 1).cuda()
     with pytest.raises(ValueError, match="stream"):
         w4.w4kv_attention(Q, p.device(w4), *p.batch([1]), stream=Foreign())
+
+
+def test_single_rows_and_heads_of_any_stride(w4):
+    """Dimensions of size one keep odd strides through torch's views."""
+    D = 64
+    p = R.Plain([40], R.INT8, 1, D, 16, 1)
+    cache, batch = p.device(w4), p.batch([1])
+    q = rows((1, 1, D), torch.float16, 3).cuda()
+    odd = q.view(D, 1).T.unsqueeze(1)
+    odd = odd.as_strided((1, 1, D), (1, 3, 1))
+    assert torch.equal(w4.w4kv_attention(odd, cache, *batch), w4.w4kv_attention(q, cache, *batch))
+    K, V = w4.w4kv_read(cache, *batch, 1)
+    other = R.Plain([40], R.INT8, 1, D, 16, 9).device(w4)
+    w4.w4kv_append(K.as_strided((1, 1, D), (5, 1, 1)), V, other, *batch)
+    k, v = w4.w4kv_read(other, *batch, 1)
+    again = R.Plain([40], R.INT8, 1, D, 16, 9).device(w4)
+    w4.w4kv_append(K, V, again, *batch)
+    assert all(torch.equal(a, b) for a, b in zip((k, v), w4.w4kv_read(again, *batch, 1)))

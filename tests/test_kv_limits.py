@@ -30,3 +30,18 @@ def test_table_width(lib, page, width, ok):
         else:
             assert status == w4.W4_ERR_INVALID_ARG
             assert b"table_width" in lib.w4_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(rows=1, krs=1, vrs=3), dict(rows=1, krs=-5, vrs=1 << 40)])
+def test_stride_of_a_single_row(lib, kw):
+    """A dimension of size one has any stride (torch gives such views)."""
+    for name in ("w4kv_append", "w4kv_read"):
+        assert rows_call(lib, name, **kw) == w4.W4_ERR_CUDA  # past the checks
+    assert attn_call(lib, rows=1, qrs=kw["krs"], ors=kw["vrs"]) == w4.W4_ERR_CUDA
+
+
+def test_stride_of_a_single_head(lib):
+    c = cache(kv_heads=1)
+    for name in ("w4kv_append", "w4kv_read"):
+        assert rows_call(lib, name, c=c, krs=128, khs=1, vrs=128, vhs=-1) == w4.W4_ERR_CUDA
+    assert attn_call(lib, c=c, heads=1, qrs=128, qhs=1, ors=128, ohs=2) == w4.W4_ERR_CUDA

@@ -355,6 +355,8 @@ int check_rows(const char *fn, const void *p, int64_t rows, int heads, int dim, 
                int64_t head_stride, bool output) {
     if (!p) return set_error(W4_ERR_INVALID_ARG, fn, "null pointer");
     const int64_t lim = int64_t(1) << 31;
+    if (rows == 1) row_stride = 0;  // of no effect
+    if (heads == 1) head_stride = 0;
     if (row_stride < 0 || head_stride < 0 || row_stride > lim || head_stride > (int64_t(1) << 40))
         return set_error(W4_ERR_INVALID_ARG, fn, "stride out of range");
     if (output) {
