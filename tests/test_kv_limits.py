@@ -45,3 +45,9 @@ def test_stride_of_a_single_head(lib):
     for name in ("w4kv_append", "w4kv_read"):
         assert rows_call(lib, name, c=c, krs=128, khs=1, vrs=128, vhs=-1) == w4.W4_ERR_CUDA
     assert attn_call(lib, c=c, heads=1, qrs=128, qhs=1, ors=128, ohs=2) == w4.W4_ERR_CUDA
+
+
+@pytest.mark.parametrize("scale,ok", [(3e38, False), (-3e38, False), (2.3e38, True), (float("nan"), False), (0.0, True)])
+def test_scale_in_base_two(lib, scale, ok):
+    """A finite scale whose product with log2(e) is not would answer NaN."""
+    assert attn_call(lib, scale=scale) == (w4.W4_ERR_CUDA if ok else w4.W4_ERR_INVALID_ARG)

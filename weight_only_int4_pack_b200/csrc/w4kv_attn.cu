@@ -159,7 +159,9 @@ int w4kv_attention(const w4kv_cache *cache, const w4kv_batch *batch, const void 
     if (heads < 1 || heads % a.c.heads != 0)
         return set_error(W4_ERR_INVALID_ARG, fn, "heads must be a multiple of kv_heads");
     if (max_rows < 1) return set_error(W4_ERR_INVALID_ARG, fn, "max_rows must be positive");
-    if (!isfinite(scale)) return set_error(W4_ERR_INVALID_ARG, fn, "scale is not finite");
+    a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    if (!isfinite(a.scale_log2))
+        return set_error(W4_ERR_INVALID_ARG, fn, "scale * log2(e) is not finite");
     if (window < 0 || (window > 0 && !causal))
         return set_error(W4_ERR_INVALID_ARG, fn, "window must be >= 0, and 0 unless causal");
     if (rows == 0 || a.b.n == 0) return W4_OK;
@@ -186,7 +188,6 @@ int w4kv_attention(const w4kv_cache *cache, const w4kv_batch *batch, const void 
     a.lse = lse;
     a.rows = rows, a.max_rows = max_rows;
     a.heads = heads, a.group = heads / a.c.heads;
-    a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
     a.causal = causal != 0;
     a.window = window > 0x7FFFFFFF ? 0 : static_cast<int>(window);
     a.page_magic = page_magic(a.c.page);
