@@ -281,3 +281,25 @@ def test_windows_of_31_bits(w4, n, window):
     batch = p.batch([n, n, n])
     want = w4.w4kv_attention(Q, p.device(w4), *batch)
     assert torch.equal(w4.w4kv_attention(Q, p.device(w4), *batch, window=window), want)
+
+
+@pytest.mark.parametrize("near", [-200.0, 0.0, 100.0, 250.0])
+@pytest.mark.parametrize("apart", [100, 128, 150, 300, 600, 1000, 1100])
+@pytest.mark.parametrize("n,H", [(40, 4), (300, 4)])
+def test_first_tokens_at_middle_distances(w4, n, H, apart, near):
+    """As above where the distance leaves nothing of the first tokens (2^-126 and
+    less), around the longest that the maximum moves by, with scores of any size."""
+    L, D, far = 900, 64, 500
+    p = R.Plain([L], R.INT8, 2, D, 16, 1, dtype=torch.bfloat16)
+    Q = rows((n, H, D), torch.bfloat16, 2)
+    Q[..., :8] = 1.0
+    unit = 1 / (8 * D ** -0.5 * 1.4427)  # in the first 8 elements of a key: a score of 1 in base 2
+    key = p.kv[0][0].copy()
+    key[:, :, :8] = near * unit
+    key[:far, :, 8:] = 0
+    key[:far, :, :8] -= apart * unit
+    p.store(0, 0, 0, *R.quantize(key, R.INT8))
+    for copies in COPIES:
+        O, lse = w4.w4kv_attention(Q.cuda().repeat(copies, 1, 1), p.device(w4), *shared(p, n, copies),
+                                   max_rows=n, return_lse=True)
+        close_copies(O, lse, R.attention(p, Q, [n], D ** -0.5, unseen=[(0, j) for j in range(far)]), copies)

@@ -825,15 +825,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                     float top = kNone;
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(unpack2(y[i]).x, unpack2(y[i]).y));
-                                    float f = 1.f;
-                                    if (far) {
-                                        m = top;
-                                    } else if (sum > 256.f) {
-                                        const float up = ceilf(top);
-                                        f = ex2(-up);
-                                        m = up < 1024.f ? m + up : 0.f;
-                                    }
-                                    far = !far && f < 0x1p-126f;
+                                    const bool over = !far && sum > 256.f;
+                                    const float up = over ? ceilf(top) : 0.f, f = ex2(-up);
+                                    m = far ? top : m + up;
+                                    far = up >= 1024.f;
+                                    if (far) m = 0.f;  // the chunk's bases are its scores then
                                     l *= f;
                                     lsum *= f;
                                     ok = rescale(f, 8 * c);
