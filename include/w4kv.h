@@ -152,9 +152,10 @@ size_t w4kv_attention_workspace_bytes(const w4kv_cache *cache, int64_t batch, in
  *   Q and what the cache's visible rows stand for must be finite for a finite
  *   result, and keys below 1e34.  Deterministic: repeated calls give the same bits.
  *   Sequences with at most 64 (row, query head) pairs per key/value head run on
- *   warp-level MMAs, bound by reading the cache; longer chunks on tcgen05.  One
- *   to four kernels, no host synchronization; a captured call follows changed
- *   lengths, pages and row counts (up to max_rows).
+ *   warp-level MMAs, bound by reading the cache; longer chunks on tcgen05.  Two
+ *   kernels, or four where max_rows allows both kinds; no host synchronization;
+ *   a captured call follows changed lengths, pages and row counts (up to
+ *   max_rows).
  *   workspace: at least w4kv_attention_workspace_bytes(...) bytes, 256-byte
  *   aligned, contents irrelevant (clobbered); one per call in flight.
  */

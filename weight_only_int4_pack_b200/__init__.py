@@ -682,7 +682,8 @@ def w4kv_attention(Q, cache: W4KVCache, page_table, kv_lens, cu_rows, max_rows=N
     tokens of each row's sequence; scale defaults to head_dim ** -0.5.  causal:
     a row sees the positions up to its own, the last `window` of them if
     window > 0.  max_rows is (at least) the longest cu_rows[b + 1] -
-    cu_rows[b]: pass 1 for a decode step; the default is the number of rows.
+    cu_rows[b]: pass 1 for a decode step; the default is the number of rows,
+    which for a batch selects slower kernels and more scratch space.
     Returns O, or (O, lse) with lse [rows][heads] fp32.
 
     Scratch space comes from the caching allocator, call by call, unless

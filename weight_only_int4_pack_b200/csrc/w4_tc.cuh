@@ -1,5 +1,5 @@
-// w4_tc.cuh -- device-side wrappers shared by the tcgen05 GEMM kernels
-// (w4_prefill.cu, w8_gemm.cu): mbarriers with bounded waits, TMA tile loads,
+// w4_tc.cuh -- device-side wrappers shared by the tcgen05 kernels
+// (w4_prefill.cu, w8_gemm.cu, w4kv_attn_tiled.cu): mbarriers with bounded waits, TMA tile loads,
 // tcgen05 fences, the 128-byte-swizzle shared-memory descriptor, MMA commit
 // and the tensor-memory load wait.  Inline PTX; sm_100a.
 #pragma once

@@ -1,11 +1,12 @@
 // w4kv_attn.cu -- w4kv_attention: argument checks, the choice of kernels, and
 // the join of partial results (semantics: include/w4kv.h).
 //
-// Sequences with at most 16 (row, query head) pairs per key/value head go to
-// the row kernel (w4kv_attn_rows.cu), all others to the tiled one
+// Sequences with at most kRowsLimit (row, query head) pairs per key/value head go
+// to the row kernel (w4kv_attn_rows.cu), all others to the tiled one
 // (w4kv_attn_tiled.cu).  The numbers of rows live on the device, so the host
 // launches what max_rows and the batch allow, and each kernel leaves out the
-// other's sequences.
+// other's sequences; a batch of one that may pass the limit goes to the tiled
+// kernel, whatever its length.
 
 #include <math.h>
 

@@ -6,11 +6,12 @@
 // of a sequence; in the tiled kernel, of a tile of its rows), plus kItemCost
 // per item for its queries and its output: positions kItemCost + u for unit u,
 // the first unit standing for the positions before it too.  The positions of
-// all items, in the order (sequence, tile, head), are cut into equal ranges, one
+// all items, in the order (sequence, head, tile), are cut into equal ranges, one
 // per block; an item that a cut divides is finished by combine_kernel from the
 // partial results of its blocks, in block order (deterministic).  The lengths
 // live on the device, so every block finds its range itself: a block-wide sum
-// over the sequences, then a scan of the 256 that hold its first unit.
+// over the sequences, then a scan of those, as many as it has threads, that hold
+// its first unit.
 #pragma once
 
 #include <float.h>
@@ -23,7 +24,7 @@ namespace w4 {
 namespace kv {
 
 constexpr int kUnit = 128;    // cached tokens per unit of work
-// What an item costs beside its units, in units.  Measured with 2, 3, 4 and 8: a
+// What an item costs beside its units, in units.  Measured on the device with 2, 3, 4 and 8: a
 // decode step of 32 sequences to 4096 (INT4) 107, 111, 113 and 122 us, 5 proposals of
 // 16 to 8000 (INT8) 72, 69, 69 and 73, chunks and single tokens mixed 208, 202, 207 and 204.
 constexpr int kItemCost = 3;
@@ -253,7 +254,7 @@ int launch_combine(const Attn &a, int grid, int tile, int dim, int xt, cudaStrea
 constexpr int kTiledRows = 256;
 int launch_tiled_attention(const Attn &a, int fmt, int dim, int xt, int grid, cudaStream_t stream);
 
-// Items of up to 16 (row, head) pairs: warp-level MMA (w4kv_attn_rows.cu).
+// Items of 8 or 16 (row, head) pairs, `tile`: warp-level MMA (w4kv_attn_rows.cu).
 constexpr int rows_blocks_per_sm(int tile) { return tile == 8 ? 4 : 2; }
 int launch_rows_attention(const Attn &a, int fmt, int dim, int xt, int tile, int grid,
                           cudaStream_t stream);

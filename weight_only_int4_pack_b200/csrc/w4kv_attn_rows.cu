@@ -9,9 +9,10 @@
 // INT4, which saves half of the shifts.  (The fp16 subnormals u * 2^-24, with the
 // zero points taken off the sums, would save the subtraction, but the MMA aligns
 // them as if they were 2^-14: errors of 2^-14 of the largest product.)  m moves
-// only when a score exceeds it by 8 (2^8 in the weights), so that O is rarely rescaled; p <= 2^8 then, and the value scales are
-// taken relative to 2^k > the running maximum / 2^7 of those that the row sees, so
-// that a weight fits fp16 (below 2^15) with 21 bits of range under the largest one.
+// only when a score exceeds it by 8 (2^8 in the weights), so that O is rarely
+// rescaled; p <= 2^8 then, and the value scales are taken relative to 2^k > the
+// running maximum / 2^7 of those that the row sees, so that a weight fits fp16
+// (below 2^15) with 21 bits of range under the largest one.
 //
 // HBM bounds it: a token of a head is 2 (dim + 4) bytes (INT8) and a few
 // thousand multiplications.  The layout keeps the shared-memory and register
@@ -32,11 +33,12 @@
 // results in shared memory at the item's end, and prefetches across items; 16
 // warps an SM (8 with tiles of 16 query rows) hide the chain of a tile.
 //
-// Measured: 64 sequences to 16384 tokens, 64 / 8 heads x 128, E4M3: 177 us, 5.65 TB/s
-// (0.86 of a copy's rate; the loads alone take 155 us); 32 sequences to 4096, 32 heads,
-// INT4: 111 us, bound by about 400 instructions per tile at half the bytes (two
-// tiles at a time per warp took the same time).  1 sequence at 1000 tokens: 8 us, and 4 for
-// the join.
+// Measured (device time): 64 sequences to 16384 tokens, 64 / 8 heads x 128, E4M3:
+// 178 us, 5.6 TB/s (0.86 of a copy's rate; the loads alone take 155 us); 32 sequences
+// to 4096, 32 heads, INT4: 110 us, bound by about 400 instructions per tile at half the
+// bytes (two tiles at a time per warp took the same time); 5 proposals of 16 sequences
+// to 8000, 8 heads per key/value head, INT8: 70 us.  1 sequence at 1000 tokens: 9.5 us,
+// and 4 for the join.
 
 #include <cuda_fp16.h>
 #include <math.h>

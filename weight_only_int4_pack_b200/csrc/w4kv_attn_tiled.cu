@@ -23,14 +23,19 @@
 // A and B; 18 prepares the steps' scales.  A stream's MMAs are S(0), then per
 // step O, S(next): while its softmax runs the tensor cores work on the other's.
 //
+// The softmax takes one pass over S in the common case; masks, moving maxima and
+// references of the rows' own share a second one, so that the common one's code
+// stays small (with the rare paths inside it: 2% on long chunks, 4% on short ones).
+//
 // What bounds it: a step needs 2048 cycles of tensor cores (2 tiles x 2 x 128 x 128 x
-// dim / 4096 a cycle at dim 128) and 2048 of exp2 (16 a cycle), and takes about 6000,
-// the chain scores -> softmax (3500 - 4100; 2480 for both streams with idle tensor
-// cores, whose operand reads compete with the loads of the scales) -> MMA warp awake
-// (300) -> O and S issued (1100 - 1600) -> S complete (700), which two streams
-// overlap in part.  Measured: 2048 rows at 16384 tokens, 64 / 8 heads x 128, E4M3:
-// 1.64 ms, 628 TFLOP/s; 509 rows at 4096, 32 heads, INT8: 108 us.  Widening alone
-// with the MMAs runs at 1300 TFLOP/s.  Every mbarrier wait is bounded.
+// dim / 4096 a cycle at dim 128) and 2048 of exp2 (16 a cycle), and takes 7500 to 8000,
+// the chain scores -> softmax (about half of it; the tensor cores' operand reads
+// compete with its loads of the scales) -> MMA warp awake -> O and S issued -> S
+// complete, which two streams overlap in part.  The softmax role spills some at 160
+// registers.  Measured (device time): 2048 rows at 16384 tokens, 64 / 8 heads x 128,
+// INT8: 1.67 ms, 618 TFLOP/s, E4M3 1.75, INT4 1.92; 509 rows at 4096, 32 heads, INT8:
+// 106 us.  Widening alone with the MMAs runs at 1300 TFLOP/s.  Every mbarrier wait is
+// bounded.
 
 #include <cuda_fp16.h>
 #include <math.h>
