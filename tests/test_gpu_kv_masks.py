@@ -303,3 +303,28 @@ def test_first_tokens_at_middle_distances(w4, n, H, apart, near):
         O, lse = w4.w4kv_attention(Q.cuda().repeat(copies, 1, 1), p.device(w4), *shared(p, n, copies),
                                    max_rows=n, return_lse=True)
         close_copies(O, lse, R.attention(p, Q, [n], D ** -0.5, unseen=[(0, j) for j in range(far)]), copies)
+
+
+@pytest.mark.parametrize("D", (64, 128))
+@pytest.mark.parametrize("up", [12, 18, 22])
+@pytest.mark.parametrize("n,H", [(3, 2), (40, 4), (300, 4)])
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_weights_before_a_long_move(w4, fmt, n, H, up, D):
+    """A token that weighs 2^-up of a later one of the same 128 keeps its part
+    where the maximum moves by more than that, past fp16's range."""
+    L = 900
+    p = R.Plain([L], fmt, 2, D, 16, 1, dtype=torch.bfloat16)
+    Q = rows((n, H, D), torch.bfloat16, 2)
+    Q[..., :8] = 1.0
+    unit = 1 / (8 * D ** -0.5 * 1.4427)  # in the first 8 elements of a key: a score of 1 in base 2
+    key = np.zeros((L, 2, D), np.float32)
+    key[600, :, :8] = 7 * unit
+    key[630, :, :8] = (7 + up) * unit
+    p.store(0, 0, 0, *R.quantize(key, fmt))
+    value = np.zeros((L, 2, D), np.float32)
+    value[600] = 1000 * np.random.default_rng(1).standard_normal((2, D))
+    p.store(1, 0, 0, *R.quantize(value, fmt))
+    for copies in COPIES:
+        O, lse = w4.w4kv_attention(Q.cuda().repeat(copies, 1, 1), p.device(w4), *shared(p, n, copies),
+                                   max_rows=n, return_lse=True)
+        close_copies(O, lse, row_tolerance(p, Q, [n], D ** -0.5), copies)

@@ -698,16 +698,16 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                                 }
                             }
                             tmem_wait_st();
-                            const __half2 f2 = __float2half2_rn(f);  // a power of two where cols > 0
 #pragma unroll 1
                             for (int c = 0; c < cols; c += 8) {
                                 uint32_t p[8];
                                 tmem_ld8(s_col + c, p);
                                 tmem_wait_ld8(p);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&p[i]), f2);
-                                    p[i] = *reinterpret_cast<const uint32_t *>(&x);
+                                for (int i = 0; i < 8; ++i) {  // (in fp32: f may be below fp16's range)
+                                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&p[i]));
+                                    const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
+                                    p[i] = *reinterpret_cast<const uint32_t *>(&y);
                                 }
                                 tmem_st8(s_col + c, p);
                             }
