@@ -227,6 +227,30 @@ def test_nan_codes_in_long_and_cut_items(w4):
         assert torch.equal(got[~nan], want[~nan])
 
 
+@pytest.mark.parametrize("D", (64, 128))
+@pytest.mark.parametrize("n,H", [(9, 22), (16, 16), (5, 16), (40, 22)])
+@pytest.mark.parametrize("fmt", R.FORMATS)
+def test_unseen_sizes_beside_wide_values(w4, fmt, n, H, D):
+    """As test_unseen_sizes, where most weights are below fp16's normal range, so
+    that any other reference of the value scales shows."""
+    L, copies = 400, 30
+    for seed in range(6):
+        r = np.random.default_rng(seed)
+        p = R.Plain([L], fmt, 2, D, 16, seed, dtype=torch.bfloat16)
+        v = r.standard_normal((L, 2, D)) * 10.0 ** r.uniform(-5, 5, (L, 1, 1))
+        p.store(1, 0, 0, *R.quantize(v.astype(np.float32), fmt))
+        Q = rows((n * copies, H, D), torch.bfloat16, seed, 2.0).cuda()
+        batch = shared(p, n, copies)
+        want = w4.w4kv_attention(Q, p.device(w4), *batch, max_rows=n)
+        for at in (L - n + 1, L - n // 2, L - 1):
+            sees = token_rows(L, n, at, 0).cuda().repeat(copies)
+            pg, off = (int(x) for x in p.at(0, at))
+            bad = p.device(w4)
+            bad.v_scales[pg, 0, off] = 1e30
+            got = w4.w4kv_attention(Q, bad, *batch, max_rows=n)
+            assert torch.equal(got[~sees], want[~sees]), (seed, at)
+
+
 # ---- scores far below zero --------------------------------------------------------------------
 
 @pytest.mark.parametrize("D", (64, 128))

@@ -202,7 +202,7 @@ struct alignas(16) Control {
     float stat[2][2][kM];           // [stream][maximum, sum][row], to join split streams
     int row_vexp[2][kM];            // [stream][row]: the row's own vexp, while a warp's rows differ
     // Largest exponent field (at least 7) of the value scales of the segment's tokens so far that
-    // all rows of the item see; -1 if the step has larger ones, that not all see.
+    // all rows of the item see; negated if the step has larger ones, that not all see.
     int vexp[kScaleStages];
     uint8_t vgroup[kScaleStages][8];  // then: the largest of each 16 tokens
     uint32_t bad[kScaleStages];     // bit i: tokens 16 i .. 16 i + 15 have no page
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                         bool own_ref = false;  // rows' references differ from the step's
                         if (ve != vcur || ve < 0) {
                             const int old = vcur < 0 ? sm->row_vexp[t][row] : vcur;
-                            int e = max(old, ve);
+                            int e = max(old, abs(ve));
                             if (ve < 0) {
 #pragma unroll 1
                                 for (int c = 0; c < 8; ++c) {
@@ -1286,7 +1286,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiled_kernel(const Attn a) {
                 if ((lane & 15) == 0) sm->vgroup[sc][2 * i + (lane >> 4)] = static_cast<uint8_t>(e[i]);
             }
             if (lane == 0) {
-                sm->vexp[sc] = own_ref ? -1 : static_cast<int>(vexp);
+                sm->vexp[sc] = own_ref ? -static_cast<int>(vexp) : static_cast<int>(vexp);
                 sm->bad[sc] = info & 255u;
                 if (info & 255u) atomicOr(a.status, kStatusBounds);
             }
